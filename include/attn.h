@@ -18,7 +18,8 @@
  *     binding checks every tensor's shape, dtype and device before it calls in).
  *   - The compute entry points (attn_fwd, attn_fwd_alibi, attn_bwd, attn_bwd_alibi,
  *     attn_quantize_fp8, attn_fwd_fp8, attn_blockmap, attn_decode_splitkv, attn_decode_paged,
- *     attn_decode_merge) are asynchronous on `stream`; they never synchronise, never allocate
+ *     attn_decode_merge, attn_page_tables, attn_qk_norm_rope, attn_qk_norm_rope_bwd,
+ *     attn_qk_norm_rope_paged, attn_decode_tree) are asynchronous on `stream`; they never synchronise, never allocate
  *     and keep no state across calls except a per-process cache of device attributes, so
  *     they may be recorded into a CUDA graph with fixed shapes ("CUDA 그래프와의 호환성").
  *     attn_get_device_status and attn_set_wait_limit_ns synchronise.
@@ -283,6 +284,146 @@ ATTN_API int attn_decode_paged(const void* q, const void* k_pages, const void* v
  */
 ATTN_API int attn_decode_merge(const float* o_part, const float* lse_part, void* o, float* lse,
                       long long rows, int num_splits, int d, cudaStream_t stream);
+
+/*
+ * attn_page_tables -- one step's bookkeeping of a paged cache, built on the GPU from the
+ * request lengths: the pages each sequence takes, its block-table row, and for every new
+ * token its slot in the cache and its position.  The outputs feed attn_qk_norm_rope_paged
+ * (slots, positions), attn_decode_paged and attn_decode_tree (block_table, seq_lens,
+ * token_offsets).  With cap = max_pages_per_seq * page_size, for sequence b in order:
+ *   c = ctx_lens[b] clamped to [0, cap]         rows in the cache before the step
+ *   token_offsets[b] = min(sum of max(new_lens, 0) before b, num_tokens); n = their difference
+ *   seq_lens[b] = min(c + n, cap)
+ *   pages: the sequence owns ceil(c / page_size) table entries and takes
+ *     ceil(seq_lens[b] / page_size) - that many more, the next entries of free_pages after
+ *     free_used[0] (0 if free_used is NULL) and after the sequences before b; they are written
+ *     to its block-table row, -1 where the free list has ended.  The other entries of the row
+ *     stay as they are.
+ *   token i of b goes to row c + i:  slots = page * page_size + (c + i) mod page_size, -1 for
+ *     a row past cap or without a page; positions = c + i, or with parents (a drafted tree,
+ *     see attn_decode_tree) c + depth, a node without a parent having depth 0.
+ *   Tokens from token_offsets[B] on are padding: slot -1, position 0.
+ *   pages_used[0] = free_used + all pages taken: what the next call's free_used is.  It is
+ *     above num_free if the list was too short, by the pages that were missing.
+ *
+ *   ctx_lens, new_lens  int32 [B]           free_pages  int32 [num_free]
+ *   free_used   int32 [1] or NULL           parents     int32 [num_tokens] or NULL
+ *   block_table int32 [B, max_pages_per_seq] (updated)
+ *   slots       int64 [num_tokens], positions int32 [num_tokens]   (written; 16-byte aligned,
+ *               the int32 arrays 4-byte aligned)
+ *   seq_lens int32 [B], token_offsets int32 [B + 1], pages_used int32 [1]   (written)
+ *   num_tokens  capacity of slots and positions; tokens beyond it get no place
+ * An output may not overlap an input or another output (INVALID_ARG): to chain steps, give
+ * seq_lens and pages_used of one step to the next as ctx_lens and free_used, and other
+ * arrays to write.
+ * Errors: INVALID_ARG, UNSUPPORTED (B > 16384; cap >= 2^31), MISALIGNED, CUDA.
+ */
+ATTN_API int attn_page_tables(const int* ctx_lens, const int* new_lens, const int* free_pages,
+             const int* free_used, const int* parents, int* block_table, long long* slots,
+             int* positions, int* seq_lens, int* token_offsets, int* pages_used, int B,
+             int max_pages_per_seq, int page_size, int num_free, int num_tokens,
+             cudaStream_t stream);
+
+/*
+ * attn_qk_norm_rope -- from the projection's output to the inputs of attn_fwd in one pass:
+ * RMS norm of every query and key head, the rotary position rotation, and the layout.
+ * A head's row x of d values becomes, with gain w and cos, sin of the token's position,
+ *   z = x w / sqrt(mean(x^2) + eps),   (y_a, y_b) = (z_a cos - z_b sin, z_b cos + z_a sin)
+ * over the pairs of the first rot values; values from rot on are z.  V rows are copied.
+ *
+ *   qkv      bf16 [B, N, Hq + 2 Hkv, d]: a token's query heads, then its key, then its value
+ *            heads; d 64 or 128
+ *   q        bf16 [B, Hq, N, d]   k, v  bf16 [B, Hkv, N, d]   (written)
+ *   q_weight, k_weight   bf16 [d]; both NULL: no norm, z = x
+ *   rope_table  fp32 [table_rows, rot], row p: cos of the rot / 2 angles of position p, then
+ *            their sin (compute the angles in 64 bits: those of far positions do not fit 32).
+ *            rot a multiple of 16, at most d; 0: no rotation
+ *   positions   int32 [B, N], or NULL: row n has position n.  A position outside
+ *            [0, table_rows) reads a table row of zeros.
+ *   interleaved 0: pair i is (i, i + rot / 2); else (2 i, 2 i + 1)
+ *   eps      > 0 (with a norm)
+ * Statistics and products are fp32, outputs rounded once.
+ * Errors: INVALID_ARG, UNSUPPORTED (d; rot), MISALIGNED, CUDA.
+ */
+ATTN_API int attn_qk_norm_rope(const void* qkv, const void* q_weight, const void* k_weight,
+             const float* rope_table, const int* positions, void* q, void* k, void* v, int B,
+             int N, int Hq, int Hkv, int d, int rot, int table_rows, float eps, int interleaved,
+             cudaStream_t stream);
+
+/*
+ * attn_qk_norm_rope_bwd -- its backward pass: from dq, dk, dv (as attn_bwd writes them) and
+ * qkv the gradients dqkv, and dq_weight, dk_weight summed over all rows of their heads.
+ *   dq       bf16 [B, Hq, N, d]   dk, dv  bf16 [B, Hkv, N, d]
+ *   dqkv     bf16 [B, N, Hq + 2 Hkv, d] (written)
+ *   dq_weight, dk_weight   fp32 [d] (written; unused without a norm)
+ *   workspace   device, 16-byte aligned, attn_qk_norm_rope_bwd_workspace_bytes(d) bytes (not
+ *            needed without a norm); contents are scratch
+ * The norm's statistics are recomputed from qkv.  Sums are taken in a fixed order: the same
+ * inputs give the same bits on the same GPU model.  Every other argument and the errors as
+ * attn_qk_norm_rope, plus WORKSPACE.
+ */
+ATTN_API size_t attn_qk_norm_rope_bwd_workspace_bytes(int d);
+ATTN_API int attn_qk_norm_rope_bwd(const void* qkv, const void* q_weight, const void* k_weight,
+             const float* rope_table, const int* positions, const void* dq, const void* dk,
+             const void* dv, void* dqkv, float* dq_weight, float* dk_weight, int B, int N, int Hq,
+             int Hkv, int d, int rot, int table_rows, float eps, int interleaved,
+             void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * attn_qk_norm_rope_paged -- the serving form: packed tokens, K and V rows written straight
+ * into the pages of the cache that attn_decode_paged and attn_decode_tree read.
+ *   qkv      bf16 [T, Hq + 2 Hkv, d]        q  bf16 [T, Hq, d] (written)
+ *   positions int32 [T]                     slots  int64 [T], 8-byte aligned
+ *   k_pages, v_pages  bf16 [num_pages, Hkv, page_size, d]: token t's rows go to row
+ *            slots[t] mod page_size of page slots[t] / page_size.  A slot outside
+ *            [0, num_pages * page_size) writes nothing; all other rows stay as they are.  Of
+ *            tokens with the same slot any one's values may end up there, and not
+ *            necessarily the same one's in every head.
+ * Every other argument and the errors as attn_qk_norm_rope, plus UNSUPPORTED for
+ * num_pages * page_size >= 2^31.
+ */
+ATTN_API int attn_qk_norm_rope_paged(const void* qkv, const void* q_weight, const void* k_weight,
+             const float* rope_table, const int* positions, const long long* slots, void* q,
+             void* k_pages, void* v_pages, int T, int Hq, int Hkv, int d, int num_pages,
+             int page_size, int rot, int table_rows, float eps, int interleaved,
+             cudaStream_t stream);
+
+/*
+ * attn_decode_tree -- attention of drafted tokens over a paged cache, for verifying a draft
+ * in one step: several query tokens a sequence, arranged as a tree, each of which sees the
+ * sequence's context, its ancestors and itself.
+ * The tokens of sequence b are rows [token_offsets[b], token_offsets[b + 1]) of q, n of them;
+ * their K and V are the LAST n of the sequence's seq_lens[b] cache rows, in the same order.
+ * Node i sees the rows [0, seq_lens[b] - n), and row seq_lens[b] - n + j for j = i and for
+ * every ancestor j of i.
+ *
+ *   q        bf16 [T, Hq, d]                o  bf16 [T, Hq, d], lse fp32 [T, Hq] (written)
+ *   k_pages, v_pages, block_table, page_size, max_pages_per_seq, seq_lens   as
+ *            attn_decode_paged (a page index outside [0, num_pages) reads zeros; lengths are
+ *            clamped)
+ *   token_offsets  int32 [B + 1], non-decreasing, in [0, T]
+ *   parents  int32 [T]: the index, within the sequence, of the node a token hangs on, or -1
+ *            for one that follows the context.  A parent comes before its node; any other
+ *            entry counts as -1.  NULL: a chain, node i hangs on i - 1 (causal)
+ *   max_nodes  largest n of the call, at most 128; of a longer sequence only the first
+ *            max_nodes tokens are computed
+ *   workspace, workspace_bytes  device scratch, 16-byte aligned, of
+ *            attn_decode_tree_workspace_bytes bytes
+ * Rows of q behind token_offsets[B], and between a sequence's max_nodes and its end, are
+ * left as they were in o and lse.  A node that sees no row (seq_lens below n) gets O = 0 and
+ * LSE = -inf.  What a page holds past the sequence's end is not used, whatever it is; rows
+ * inside the length take part in one product for all nodes of the sequence, so a NaN or
+ * infinity in V there may reach nodes that do not see its row.
+ * Hq / Hkv <= 16, d in {64, 128}, page_size a multiple of 64.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, CUDA.
+ */
+ATTN_API size_t attn_decode_tree_workspace_bytes(int B, int Hq, int Hkv, int max_nodes, int d,
+             int device);
+ATTN_API int attn_decode_tree(const void* q, const void* k_pages, const void* v_pages,
+             const int* block_table, const int* seq_lens, const int* token_offsets,
+             const int* parents, void* o, float* lse, int B, int T, int Hq, int Hkv,
+             int num_pages, int page_size, int max_pages_per_seq, int max_nodes, int d,
+             float scale, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * attn_get_device_status -- synchronises `stream`, then returns and clears the device-side

@@ -52,6 +52,15 @@ SIGNATURES = {
                                             c_void_p]),
     "attn_decode_merge": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_longlong, c_int,
                                   c_int, c_void_p]),
+    "attn_page_tables": (c_int, [c_void_p] * 11 + [c_int] * 5 + [c_void_p]),
+    "attn_qk_norm_rope": (c_int, [c_void_p] * 8 + [c_int] * 7 + [c_float, c_int, c_void_p]),
+    "attn_qk_norm_rope_bwd_workspace_bytes": (c_size_t, [c_int]),
+    "attn_qk_norm_rope_bwd": (c_int, [c_void_p] * 11 + [c_int] * 7
+                              + [c_float, c_int, c_void_p, c_size_t, c_void_p]),
+    "attn_qk_norm_rope_paged": (c_int, [c_void_p] * 9 + [c_int] * 8 + [c_float, c_int, c_void_p]),
+    "attn_decode_tree_workspace_bytes": (c_size_t, [c_int] * 6),
+    "attn_decode_tree": (c_int, [c_void_p] * 9 + [c_int] * 9
+                         + [c_float, c_void_p, c_size_t, c_void_p]),
     "attn_get_device_status": (c_int, [c_void_p]),
     "attn_last_error_site": (c_int, []),
     "attn_set_wait_limit_ns": (c_int, [ctypes.c_ulonglong]),

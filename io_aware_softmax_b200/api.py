@@ -426,6 +426,281 @@ def attn_merge(o_part: torch.Tensor, lse_part: torch.Tensor, *, out: Optional[to
     return out, lse
 
 
+def _int32(t: Optional[torch.Tensor], name: str, shape, ref: torch.Tensor):
+    """Checks an optional int32 array (lengths, tables, indices)."""
+    if t is not None:
+        _need(t, name, torch.int32, len(shape))
+        _shape(t, name, shape)
+        _same_device(ref, (t, name))
+
+
+def attn_page_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor,
+                     block_table: torch.Tensor, *, page_size: int, num_tokens: int,
+                     free_used: Optional[torch.Tensor] = None,
+                     parents: Optional[torch.Tensor] = None,
+                     slots: Optional[torch.Tensor] = None,
+                     positions: Optional[torch.Tensor] = None,
+                     seq_lens: Optional[torch.Tensor] = None,
+                     token_offsets: Optional[torch.Tensor] = None,
+                     pages_used: Optional[torch.Tensor] = None, stream=None):
+    """Pages, block-table entries (block_table is updated), slots and positions of one step's
+    new tokens, from int32 lengths [B] before the step and of the step.
+
+    Returns (slots int64 [num_tokens], positions int32 [num_tokens], seq_lens int32 [B],
+    token_offsets int32 [B+1], pages_used int32 [1]).  ``parents`` (int32 [num_tokens]) gives
+    the tokens of drafted trees positions by depth; ``free_used`` is the pages_used of an
+    earlier step on the same free list."""
+    lib = _lib.load()
+    _need(ctx_lens, "ctx_lens", torch.int32, 1)
+    _need(free_pages, "free_pages", torch.int32, 1)
+    _need(block_table, "block_table", torch.int32, 2)
+    B, max_pages = ctx_lens.shape[0], block_table.shape[1]
+    T, dev = int(num_tokens), ctx_lens.device
+    if T < 0:
+        raise ValueError("num_tokens must not be negative")
+    if block_table.shape[0] != B:
+        raise ValueError("block_table needs one row per sequence")
+    _same_device(ctx_lens, (free_pages, "free_pages"), (block_table, "block_table"))
+    _int32(new_lens, "new_lens", (B,), ctx_lens)
+    _int32(free_used, "free_used", (1,), ctx_lens)
+    _int32(parents, "parents", (T,), ctx_lens)
+
+    def output(t, name, dtype, shape):
+        if t is None:
+            return torch.empty(shape, dtype=dtype, device=dev)
+        _out(t, name, dtype, shape, ctx_lens)
+        return t
+
+    slots = output(slots, "slots", torch.int64, (T,))
+    positions = output(positions, "positions", torch.int32, (T,))
+    seq_lens = output(seq_lens, "seq_lens", torch.int32, (B,))
+    token_offsets = output(token_offsets, "token_offsets", torch.int32, (B + 1,))
+    pages_used = output(pages_used, "pages_used", torch.int32, (1,))
+    with _device(ctx_lens):
+        st = lib.attn_page_tables(_ptr(ctx_lens), _ptr(new_lens), _ptr(free_pages),
+                                  _ptr(free_used), _ptr(parents), _ptr(block_table), _ptr(slots),
+                                  _ptr(positions), _ptr(seq_lens), _ptr(token_offsets),
+                                  _ptr(pages_used), B, max_pages, int(page_size),
+                                  free_pages.shape[0], T, _stream(dev, stream))
+    _check(st, "attn_page_tables")
+    return slots, positions, seq_lens, token_offsets, pages_used
+
+
+def _prep_inputs(qkv: torch.Tensor, dims: int, q_weight, k_weight, rope_table):
+    """Checks the projection's output, the gains and the angle table; returns (rot, rows)."""
+    _need(qkv, "qkv", torch.bfloat16, dims)
+    d = qkv.shape[-1]
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight are given together, or neither")
+    if q_weight is not None:
+        for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            _need(t, n, torch.bfloat16, 1)
+            _shape(t, n, (d,))
+            _same_device(qkv, (t, n))
+    if rope_table is None:
+        return 0, 0
+    _need(rope_table, "rope_table", torch.float32, 2)
+    _same_device(qkv, (rope_table, "rope_table"))
+    return rope_table.shape[1], rope_table.shape[0]
+
+
+def attn_qk_norm_rope(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
+                      k_weight: Optional[torch.Tensor], rope_table: Optional[torch.Tensor], *,
+                      num_q_heads: int, positions: Optional[torch.Tensor] = None,
+                      eps: float = 1e-6, interleaved: bool = False,
+                      q: Optional[torch.Tensor] = None, k: Optional[torch.Tensor] = None,
+                      v: Optional[torch.Tensor] = None, stream=None
+                      ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Per-head RMS norm and rotary rotation of q and k, from qkv bf16 [B,N,Hq+2*Hkv,d] to
+    (q [B,Hq,N,d], k [B,Hkv,N,d], v [B,Hkv,N,d]) as attn_fwd takes them.
+
+    Gains bf16 [d] (both None: no norm); rope_table fp32 [rows, rot], cos | sin of each
+    position's rot/2 angles (None: no rotation); positions int32 [B,N] (None: 0..N-1)."""
+    lib = _lib.load()
+    rot, rows = _prep_inputs(qkv, 4, q_weight, k_weight, rope_table)
+    B, N, H, d = qkv.shape
+    Hq = int(num_q_heads)
+    if not 0 < Hq < H or (H - Hq) % 2:
+        raise ValueError(f"{H} heads cannot be {Hq} query heads and as many key as value heads")
+    Hkv = (H - Hq) // 2
+    _int32(positions, "positions", (B, N), qkv)
+    shapes = ((B, Hq, N, d), (B, Hkv, N, d), (B, Hkv, N, d))
+    out = []
+    for t, n, shape in zip((q, k, v), "qkv", shapes):
+        if t is None:
+            t = torch.empty(shape, dtype=torch.bfloat16, device=qkv.device)
+        else:
+            _out(t, n, torch.bfloat16, shape, qkv)
+        out.append(t)
+    q, k, v = out
+    with _device(qkv):
+        st = lib.attn_qk_norm_rope(_ptr(qkv), _ptr(q_weight), _ptr(k_weight), _ptr(rope_table),
+                                   _ptr(positions), _ptr(q), _ptr(k), _ptr(v), B, N, Hq, Hkv, d,
+                                   rot, rows, float(eps), int(bool(interleaved)),
+                                   _stream(qkv.device, stream))
+    _check(st, "attn_qk_norm_rope")
+    return q, k, v
+
+
+def attn_qk_norm_rope_bwd(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
+                          k_weight: Optional[torch.Tensor], rope_table: Optional[torch.Tensor],
+                          dq: torch.Tensor, dk: torch.Tensor, dv: torch.Tensor, *,
+                          positions: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                          interleaved: bool = False, dqkv: Optional[torch.Tensor] = None,
+                          dq_weight: Optional[torch.Tensor] = None,
+                          dk_weight: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, stream=None):
+    """Backward of attn_qk_norm_rope: (dqkv bf16 as qkv, dq_weight fp32 [d], dk_weight fp32 [d])
+    from qkv and attn_bwd's (dq, dk, dv); the gains' gradients are None without a norm."""
+    lib = _lib.load()
+    rot, rows = _prep_inputs(qkv, 4, q_weight, k_weight, rope_table)
+    B, N, H, d = qkv.shape
+    for t, n in ((dq, "dq"), (dk, "dk"), (dv, "dv")):
+        _need(t, n, torch.bfloat16, 4)
+    Hq, Hkv = dq.shape[1], dk.shape[1]
+    if Hq + 2 * Hkv != H:
+        raise ValueError(f"dq and dk have {Hq} and {Hkv} heads, qkv {H}")
+    _shape(dq, "dq", (B, Hq, N, d))
+    _shape(dk, "dk", (B, Hkv, N, d))
+    _shape(dv, "dv", (B, Hkv, N, d))
+    _same_device(qkv, (dq, "dq"), (dk, "dk"), (dv, "dv"))
+    _int32(positions, "positions", (B, N), qkv)
+    if dqkv is None:
+        dqkv = torch.empty_like(qkv)
+    else:
+        _out(dqkv, "dqkv", torch.bfloat16, qkv.shape, qkv)
+    ws_bytes = 0
+    if q_weight is None:
+        if dq_weight is not None or dk_weight is not None:
+            raise ValueError("without a norm there are no gains to take gradients of")
+        workspace = None
+    else:
+        grads = []
+        for t, n in ((dq_weight, "dq_weight"), (dk_weight, "dk_weight")):
+            if t is None:
+                t = torch.empty((d,), dtype=torch.float32, device=qkv.device)
+            else:
+                _out(t, n, torch.float32, (d,), qkv)
+            grads.append(t)
+        dq_weight, dk_weight = grads
+        if workspace is None:
+            need = attn_qk_norm_rope_bwd_workspace_bytes(d)
+            workspace = torch.empty(need, dtype=torch.uint8, device=qkv.device)
+        ws_bytes = _workspace(workspace, qkv)
+    with _device(qkv):
+        st = lib.attn_qk_norm_rope_bwd(_ptr(qkv), _ptr(q_weight), _ptr(k_weight),
+                                       _ptr(rope_table), _ptr(positions), _ptr(dq), _ptr(dk),
+                                       _ptr(dv), _ptr(dqkv), _ptr(dq_weight), _ptr(dk_weight), B,
+                                       N, Hq, Hkv, d, rot, rows, float(eps),
+                                       int(bool(interleaved)), _ptr(workspace), ws_bytes,
+                                       _stream(qkv.device, stream))
+    _check(st, "attn_qk_norm_rope_bwd")
+    return dqkv, dq_weight, dk_weight
+
+
+def attn_qk_norm_rope_bwd_workspace_bytes(d: int) -> int:
+    return int(_lib.load().attn_qk_norm_rope_bwd_workspace_bytes(d))
+
+
+def attn_qk_norm_rope_paged(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
+                            k_weight: Optional[torch.Tensor],
+                            rope_table: Optional[torch.Tensor], positions: torch.Tensor,
+                            slots: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, *,
+                            eps: float = 1e-6, interleaved: bool = False,
+                            q: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """attn_qk_norm_rope for packed tokens qkv bf16 [T,Hq+2*Hkv,d]: returns q [T,Hq,d] and
+    writes the K and V rows of each token into pages [num_pages,Hkv,page_size,d] at its slot
+    (int64 [T]; a slot outside the cache writes nothing).  positions int32 [T]."""
+    lib = _lib.load()
+    rot, rows = _prep_inputs(qkv, 3, q_weight, k_weight, rope_table)
+    T, H, d = qkv.shape
+    _need(k_pages, "k_pages", torch.bfloat16, 4)
+    _need(v_pages, "v_pages", torch.bfloat16, 4)
+    num_pages, Hkv, page_size = k_pages.shape[:3]
+    _shape(k_pages, "k_pages", (num_pages, Hkv, page_size, d))
+    _shape(v_pages, "v_pages", k_pages.shape)
+    Hq = H - 2 * Hkv
+    if Hq <= 0:
+        raise ValueError(f"qkv has {H} heads: none for queries beside {Hkv} key and value heads")
+    if positions is None:
+        raise TypeError("positions must be a torch.Tensor")
+    _int32(positions, "positions", (T,), qkv)
+    _need(slots, "slots", torch.int64, 1)
+    _shape(slots, "slots", (T,))
+    _same_device(qkv, (k_pages, "k_pages"), (v_pages, "v_pages"), (slots, "slots"))
+    if q is None:
+        q = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=qkv.device)
+    else:
+        _out(q, "q", torch.bfloat16, (T, Hq, d), qkv)
+    with _device(qkv):
+        st = lib.attn_qk_norm_rope_paged(_ptr(qkv), _ptr(q_weight), _ptr(k_weight),
+                                         _ptr(rope_table), _ptr(positions), _ptr(slots), _ptr(q),
+                                         _ptr(k_pages), _ptr(v_pages), T, Hq, Hkv, d, num_pages,
+                                         page_size, rot, rows, float(eps),
+                                         int(bool(interleaved)), _stream(qkv.device, stream))
+    _check(st, "attn_qk_norm_rope_paged")
+    return q
+
+
+def attn_decode_tree_workspace_bytes(B: int, Hq: int, Hkv: int, max_nodes: int, d: int,
+                                     device: int = 0) -> int:
+    return int(_lib.load().attn_decode_tree_workspace_bytes(B, Hq, Hkv, max_nodes, d, device))
+
+
+def attn_decode_tree(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                     block_table: torch.Tensor, seq_lens: torch.Tensor,
+                     token_offsets: torch.Tensor, *, max_nodes: int,
+                     parents: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                     workspace: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                     stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of drafted trees over a paged cache: q [T,Hq,d], packed by token_offsets
+    int32 [B+1]; pages [num_pages,Hkv,page_size,d]; block_table int32 [B,max_pages]; seq_lens
+    int32 [B], the last rows of each being its drafted tokens' -> (O [T,Hq,d], LSE [T,Hq]).
+
+    parents int32 [T]: index within the sequence of the node each token hangs on, -1 for the
+    context; None: a chain.  Rows behind token_offsets[B] are left as they were."""
+    lib = _lib.load()
+    _need(q, "q", torch.bfloat16, 3)
+    T, Hq, d = q.shape
+    _need(k_pages, "k_pages", torch.bfloat16, 4)
+    _need(v_pages, "v_pages", torch.bfloat16, 4)
+    num_pages, Hkv, page_size = k_pages.shape[:3]
+    if k_pages.shape[3] != d:
+        raise ValueError(f"k_pages {tuple(k_pages.shape)} must have the head size {d} of q")
+    _shape(v_pages, "v_pages", k_pages.shape)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    B = seq_lens.shape[0]
+    _need(block_table, "block_table", torch.int32, 2)
+    if block_table.shape[0] != B:
+        raise ValueError("block_table needs one row per sequence")
+    _same_device(q, (k_pages, "k_pages"), (v_pages, "v_pages"), (block_table, "block_table"),
+                 (seq_lens, "seq_lens"))
+    _need(token_offsets, "token_offsets", torch.int32, 1)
+    _int32(token_offsets, "token_offsets", (B + 1,), q)
+    _int32(parents, "parents", (T,), q)
+    if workspace is None:
+        need = attn_decode_tree_workspace_bytes(B, Hq, Hkv, int(max_nodes), d, _index(q))
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    ws_bytes = _workspace(workspace, q)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _out(out, "out", torch.bfloat16, (T, Hq, d), q)
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    else:
+        _out(lse, "lse", torch.float32, (T, Hq), q)
+    with _device(q):
+        st = lib.attn_decode_tree(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table),
+                                  _ptr(seq_lens), _ptr(token_offsets), _ptr(parents), _ptr(out),
+                                  _ptr(lse), B, T, Hq, Hkv, num_pages, page_size,
+                                  block_table.shape[1], int(max_nodes), d, float(scale or 0.0),
+                                  _ptr(workspace), ws_bytes, _stream(q.device, stream))
+    _check(st, "attn_decode_tree")
+    return out, lse
+
+
 def device_status(stream=None, device=None) -> int:
     """Synchronises the stream and returns (and clears) the library's device error status."""
     lib = _lib.load()

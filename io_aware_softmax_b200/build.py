@@ -20,8 +20,9 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 LIB_NAME = "libattn_b200.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["attn_api.cu", "attn_prefill.cu", "attn_decode.cu", "attn_blockmap.cu",
-           "attn_decode_noalloc.cu", "attn_backward.cu", "attn_fp8.cu"]
-HEADERS = ["attn_internal.h", "mask.cuh", "sm100_ptx.cuh", "tmem_ldst.cuh", "tanh_poly.cuh"]
+           "attn_decode_noalloc.cu", "attn_backward.cu", "attn_fp8.cu",
+           "attn_pages.cu", "attn_qkprep.cu", "attn_tree.cu"]
+HEADERS = ["attn_internal.h", "attn_serve.h", "mask.cuh", "sm100_ptx.cuh", "tmem_ldst.cuh", "tanh_poly.cuh"]
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 # Kernels that split their launch registers between warpgroups with setmaxnreg (two
@@ -34,6 +35,7 @@ SPLIT_KERNELS = [
     ("attn_fwd_sm100_kernel", "attn_prefill.cu", "kRegsSoftmaxCap", "kRegsOtherCap"),
     ("attn_bwd_dq_kernel", "attn_backward.cu", "kBwdRegsElem", "kBwdRegsOther"),
     ("attn_bwd_dkdv_kernel", "attn_backward.cu", "kBwdRegsElem", "kBwdRegsOther"),
+    ("attn_tree_kernel", "attn_tree.cu", "kTreeRegsSoftmax", "kTreeRegsOther"),
 ]
 SPLIT_THREADS = 384
 PREFILL_KERNEL = SPLIT_KERNELS[0][0]

@@ -11,6 +11,7 @@
 
 #include "../../include/attn.h"
 #include "attn_internal.h"
+#include "attn_serve.h"
 #include "sm100_ptx.cuh"
 #include "tanh_poly.cuh"
 
@@ -68,6 +69,21 @@ bool make_map_3d(CUtensorMap* map, const void* ptr, int d, long long rows, long 
   cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+// Query rows of the tree attention: q [T, Hkv * G, d] as (d, G, Hkv, T) in boxes of
+// 64 x G x 1 x nodes, so one box is the rows (node, head of the group) of one KV head.
+bool make_map_tree_q(CUtensorMap* map, const void* ptr, int d, int G, int Hkv, int T, int nodes) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)G, (cuuint64_t)Hkv, (cuuint64_t)T};
+  cuuint64_t strides[3] = {(cuuint64_t)d * 2, (cuuint64_t)d * 2 * G, (cuuint64_t)d * 2 * G * Hkv};
+  cuuint32_t box[4] = {64, (cuuint32_t)G, 1, (cuuint32_t)nodes};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides,
                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
@@ -620,4 +636,293 @@ extern "C" int attn_fwd_fp8(const void* q8, const void* k8, const void* vt8,
       !make_map_3d_u8(&tv, vt8, Nk, nk_pad, d, (long long)B * Hkv, d))
     return ATTN_ERR_CUDA;
   return launch_attn_fwd(tq, tk, tv, p, d, stream) == 0 ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ page tables and slots
+
+static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && na > 0 && nb > 0 && x < y + nb && y < x + na;
+}
+
+extern "C" int attn_page_tables(const int* ctx_lens, const int* new_lens, const int* free_pages,
+                                const int* free_used, const int* parents, int* block_table,
+                                long long* slots, int* positions, int* seq_lens,
+                                int* token_offsets, int* pages_used, int B, int max_pages_per_seq,
+                                int page_size, int num_free, int num_tokens,
+                                cudaStream_t stream) {
+  if (B < 0 || max_pages_per_seq < 0 || page_size <= 0 || num_free < 0 || num_tokens < 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (B > kPagesMaxSeqs || (long long)max_pages_per_seq * page_size > (1LL << 31) - 1)
+    return ATTN_ERR_UNSUPPORTED;
+  if (!token_offsets || !pages_used || (num_tokens > 0 && (!slots || !positions)) ||
+      (B > 0 && (!ctx_lens || !new_lens || !seq_lens)) ||
+      (B > 0 && max_pages_per_seq > 0 && !block_table) || (num_free > 0 && !free_pages))
+    return ATTN_ERR_INVALID_ARG;
+  const void* ptrs[] = {slots, positions};
+  for (const void* q : ptrs)
+    if (!aligned16(q)) return ATTN_ERR_MISALIGNED;
+  const void* ints[] = {ctx_lens, new_lens, free_pages, free_used, parents,
+                        block_table, seq_lens, token_offsets, pages_used};
+  for (const void* q : ints)
+    if (reinterpret_cast<uintptr_t>(q) & 3u) return ATTN_ERR_MISALIGNED;
+  // every block reads the inputs while block 0 writes the outputs
+  const size_t nb = (size_t)B * 4, nt = (size_t)num_tokens * 4;
+  const void* ins[] = {ctx_lens, new_lens, free_pages, free_used, parents};
+  const size_t in_bytes[] = {nb, nb, (size_t)num_free * 4, 4, nt};
+  const void* outs[] = {block_table, slots, positions, seq_lens, token_offsets, pages_used};
+  const size_t out_bytes[] = {nb * max_pages_per_seq, 2 * nt, nt, nb, nb + 4, 4};
+  for (int o = 0; o < 6; ++o) {
+    for (int i = 0; i < 5; ++i)
+      if (overlap(ins[i], in_bytes[i], outs[o], out_bytes[o])) return ATTN_ERR_INVALID_ARG;
+    for (int i = 0; i < o; ++i)
+      if (overlap(outs[i], out_bytes[i], outs[o], out_bytes[o])) return ATTN_ERR_INVALID_ARG;
+  }
+  PagesParams p{ctx_lens, new_lens, free_pages, free_used, parents, block_table, slots, positions,
+                seq_lens, token_offsets, pages_used, B, max_pages_per_seq, page_size, num_free,
+                num_tokens};
+  return launch_page_tables(p, sm_count(current_device()), stream) == 0 ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// ----------------------------------------------------------- query / key norm and rotation
+
+// The checks that the three forms share; fills the common fields of p.
+static int check_prep(PrepParams& p, const void* qkv, const void* q_weight, const void* k_weight,
+                      const float* rope_table, const int* positions, long long tokens, int N,
+                      int Hq, int Hkv, int d, int rot, int table_rows, float eps,
+                      int interleaved) {
+  if (tokens < 0 || N < 0 || Hq < 0 || Hkv < 0 || rot < 0 || table_rows < 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (rot > d || rot % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+  if ((q_weight == nullptr) != (k_weight == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (q_weight != nullptr && !(eps > 0.f && eps <= 3.4e38f)) return ATTN_ERR_INVALID_ARG;
+  const long long H = (long long)Hq + 2LL * Hkv;
+  // rows of one call: a warp takes several, and their number is a 32-bit index
+  if (tokens * H > (1LL << 31) - 1 || H > (1 << 20)) return ATTN_ERR_UNSUPPORTED;
+  if (tokens > 0 && H > 0) {
+    if (qkv == nullptr || (rot > 0 && table_rows > 0 && rope_table == nullptr))
+      return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(qkv) || !aligned16(q_weight) || !aligned16(k_weight) || !aligned16(rope_table) ||
+        (reinterpret_cast<uintptr_t>(positions) & 3u))
+      return ATTN_ERR_MISALIGNED;
+  }
+  p.qkv = qkv;
+  p.wq = q_weight;
+  p.wk = k_weight;
+  p.table = rope_table;
+  p.positions = positions;
+  p.tokens = (int)tokens;
+  p.N = N;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.H = (int)H;
+  p.rot = rot;
+  p.table_rows = table_rows;
+  p.interleaved = interleaved != 0;
+  p.eps = eps;
+  return ATTN_OK;
+}
+
+extern "C" int attn_qk_norm_rope(const void* qkv, const void* q_weight, const void* k_weight,
+                                 const float* rope_table, const int* positions, void* q, void* k,
+                                 void* v, int B, int N, int Hq, int Hkv, int d, int rot,
+                                 int table_rows, float eps, int interleaved,
+                                 cudaStream_t stream) {
+  if (B < 0) return ATTN_ERR_INVALID_ARG;
+  PrepParams p{};
+  const int st = check_prep(p, qkv, q_weight, k_weight, rope_table, positions, (long long)B * N, N,
+                            Hq, Hkv, d, rot, table_rows, eps, interleaved);
+  if (st != ATTN_OK) return st;
+  if (p.tokens == 0 || p.H == 0) return ATTN_OK;
+  if ((Hq > 0 && !q) || (Hkv > 0 && (!k || !v))) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v)) return ATTN_ERR_MISALIGNED;
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  return launch_qk_prep(p, d, false, stream) == 0 ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+extern "C" int attn_qk_norm_rope_paged(const void* qkv, const void* q_weight,
+                                       const void* k_weight, const float* rope_table,
+                                       const int* positions, const long long* slots, void* q,
+                                       void* k_pages, void* v_pages, int T, int Hq, int Hkv, int d,
+                                       int num_pages, int page_size, int rot, int table_rows,
+                                       float eps, int interleaved, cudaStream_t stream) {
+  if (num_pages < 0 || page_size <= 0) return ATTN_ERR_INVALID_ARG;
+  PrepParams p{};
+  const int st = check_prep(p, qkv, q_weight, k_weight, rope_table, positions, T, 1, Hq, Hkv, d,
+                            rot, table_rows, eps, interleaved);
+  if (st != ATTN_OK) return st;
+  if ((long long)num_pages * page_size > (1LL << 31) - 1) return ATTN_ERR_UNSUPPORTED;
+  if (p.tokens == 0 || p.H == 0) return ATTN_OK;
+  if ((Hq > 0 && !q) || !positions || !slots || (Hkv > 0 && num_pages > 0 && (!k_pages || !v_pages)))
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) ||
+      (reinterpret_cast<uintptr_t>(slots) & 7u))
+    return ATTN_ERR_MISALIGNED;
+  p.q = q;
+  p.k = k_pages;
+  p.v = v_pages;
+  p.slots = slots;
+  p.page_size = page_size;
+  p.num_slots = num_pages * page_size;
+  return launch_qk_prep(p, d, true, stream) == 0 ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+extern "C" size_t attn_qk_norm_rope_bwd_workspace_bytes(int d) {
+  return d > 0 ? (size_t)kPrepBwdMaxBlocks * 2 * d * sizeof(float) : 0;
+}
+
+extern "C" int attn_qk_norm_rope_bwd(const void* qkv, const void* q_weight, const void* k_weight,
+                                     const float* rope_table, const int* positions,
+                                     const void* dq, const void* dk, const void* dv, void* dqkv,
+                                     float* dq_weight, float* dk_weight, int B, int N, int Hq,
+                                     int Hkv, int d, int rot, int table_rows, float eps,
+                                     int interleaved, void* workspace, size_t workspace_bytes,
+                                     cudaStream_t stream) {
+  if (B < 0) return ATTN_ERR_INVALID_ARG;
+  PrepBwdParams p{};
+  const int st = check_prep(p.f, qkv, q_weight, k_weight, rope_table, positions, (long long)B * N,
+                            N, Hq, Hkv, d, rot, table_rows, eps, interleaved);
+  if (st != ATTN_OK) return st;
+  const bool norm = q_weight != nullptr;
+  if (norm) {
+    if (!dq_weight || !dk_weight) return ATTN_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(dq_weight) | reinterpret_cast<uintptr_t>(dk_weight)) & 3u)
+      return ATTN_ERR_MISALIGNED;
+  }
+  if (p.f.tokens == 0 || p.f.H == 0) {      // no rows: the gains' gradients are empty sums
+    if (norm && (cudaMemsetAsync(dq_weight, 0, (size_t)d * 4, stream) != cudaSuccess ||
+                 cudaMemsetAsync(dk_weight, 0, (size_t)d * 4, stream) != cudaSuccess))
+      return ATTN_ERR_CUDA;
+    return ATTN_OK;
+  }
+  if ((Hq > 0 && !dq) || (Hkv > 0 && (!dk || !dv)) || !dqkv) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned16(dqkv))
+    return ATTN_ERR_MISALIGNED;
+  if (norm) {
+    if (workspace == nullptr || workspace_bytes < attn_qk_norm_rope_bwd_workspace_bytes(d))
+      return ATTN_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
+  }
+  p.f.q = const_cast<void*>(dq);
+  p.f.k = const_cast<void*>(dk);
+  p.f.v = const_cast<void*>(dv);
+  p.dqkv = dqkv;
+  p.partials = static_cast<float*>(workspace);
+  p.dwq = dq_weight;
+  p.dwk = dk_weight;
+  return launch_qk_prep_bwd(p, d, sm_count(current_device()), stream) == 0 ? ATTN_OK
+                                                                           : ATTN_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------------- tree attention
+
+namespace {
+
+// How a tree call is cut: nodes of a query tile, whether a CTA takes two of them, and where
+// the workspace's arrays begin.
+struct TreePlan {
+  int tile_nodes, tiles, grid;
+  size_t ml, o, bytes;
+};
+
+TreePlan tree_plan(int B, int G, int max_nodes, int d, int device) {
+  TreePlan t;
+  t.tile_nodes = std::min(kTreeRows / G, std::max(max_nodes, 1));
+  t.tiles = max_nodes > t.tile_nodes ? 2 : 1;
+  t.grid = sm_count(device);
+  const size_t rows = (size_t)2 * t.grid * t.tiles * kTreeRows;
+  t.ml = (((size_t)B + 1) * 8 + 255) & ~(size_t)255;
+  t.o = t.ml + ((rows * 8 + 255) & ~(size_t)255);
+  t.bytes = t.o + rows * d * 4;
+  return t;
+}
+
+}  // namespace
+
+extern "C" size_t attn_decode_tree_workspace_bytes(int B, int Hq, int Hkv, int max_nodes, int d,
+                                                   int device) {
+  if (B <= 0 || Hkv <= 0 || Hq < Hkv || Hq / Hkv > 16 || max_nodes <= 0 || d <= 0) return 0;
+  return tree_plan(B, Hq / Hkv, max_nodes, d, device).bytes;
+}
+
+extern "C" int attn_decode_tree(const void* q, const void* k_pages, const void* v_pages,
+                                const int* block_table, const int* seq_lens,
+                                const int* token_offsets, const int* parents, void* o, float* lse,
+                                int B, int T, int Hq, int Hkv, int num_pages, int page_size,
+                                int max_pages_per_seq, int max_nodes, int d, float scale,
+                                void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (B < 0 || T < 0 || Hq < 0 || Hkv < 0 || num_pages < 0 || page_size <= 0 ||
+      max_pages_per_seq < 0 || max_nodes < 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (page_size % 64 != 0 || max_nodes > kTreeMaxNodes) return ATTN_ERR_UNSUPPORTED;
+  if (Hkv == 0 && Hq > 0) return ATTN_ERR_INVALID_ARG;
+  if (Hkv > 0 && Hq % Hkv != 0) return ATTN_ERR_UNSUPPORTED;
+  if (std::isnan(scale)) return ATTN_ERR_INVALID_ARG;
+  if (B == 0 || T == 0 || Hq == 0 || max_nodes == 0) return ATTN_OK;
+  const int G = Hq / Hkv;
+  if (G > 16) return ATTN_ERR_UNSUPPORTED;
+  const long long cap = (long long)max_pages_per_seq * page_size;
+  if (!q || !o || !lse || !seq_lens || !token_offsets || (cap > 0 && !block_table) ||
+      (num_pages > 0 && (!k_pages || !v_pages)))
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned16(k_pages) ||
+      !aligned16(v_pages))
+    return ATTN_ERR_MISALIGNED;
+  if ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(seq_lens) |
+       reinterpret_cast<uintptr_t>(token_offsets) | reinterpret_cast<uintptr_t>(parents)) & 3u)
+    return ATTN_ERR_MISALIGNED;
+  const int dev = current_device();
+  const TreePlan plan = tree_plan(B, G, max_nodes, d, dev);
+  const long long blocks = (max_nodes + plan.tile_nodes * plan.tiles - 1) /
+                           (plan.tile_nodes * plan.tiles);
+  if (cap > (1LL << 31) - 1 - 256 || (long long)num_pages * Hkv > (1LL << 31) - 1 ||
+      (long long)T * Hq > (1LL << 31) - 1 ||
+      blocks * Hkv * std::max((cap + 127) / 128, 1LL) > (1LL << 31) - 1)
+    return ATTN_ERR_UNSUPPORTED;
+  if (workspace == nullptr || workspace_bytes < plan.bytes) return ATTN_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
+  if (scale <= 0.f) scale = 1.0f / std::sqrt((float)d);
+
+  TreeParams p{};
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.offsets = token_offsets;
+  p.parents = parents;
+  p.o = o;
+  p.lse = lse;
+  char* ws = static_cast<char*>(workspace);
+  p.prefix = reinterpret_cast<long long*>(ws);
+  p.ml_part = reinterpret_cast<float2*>(ws + plan.ml);
+  p.o_part = reinterpret_cast<float*>(ws + plan.o);
+  p.B = B;
+  p.T = T;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = G;
+  p.page_size = page_size;
+  p.max_pages = max_pages_per_seq;
+  // without a page there is no row: every length counts as 0
+  p.num_pages = num_pages;
+  p.cap = num_pages > 0 ? (int)cap : 0;
+  p.max_nodes = max_nodes;
+  p.tile_nodes = plan.tile_nodes;
+  p.grid = plan.grid;
+  p.kscale = scale * kLog2e;
+  p.err = error_word_ptr(dev);
+  if (p.err == nullptr) return ATTN_ERR_CUDA;
+  if (num_pages == 0) {      // the maps need a tensor: nothing of it is read
+    k_pages = v_pages = q;
+    p.num_pages = 0;
+  }
+  CUtensorMap tq, tk, tv;
+  const long long z = std::max((long long)num_pages * Hkv, 1LL);
+  if (!make_map_tree_q(&tq, q, d, G, Hkv, T, plan.tile_nodes) ||
+      !make_map_3d(&tk, k_pages, d, num_pages > 0 ? page_size : 1, z, 64) ||
+      !make_map_3d(&tv, v_pages, d, num_pages > 0 ? page_size : 1, z, 64))
+    return ATTN_ERR_CUDA;
+  return launch_tree(tq, tk, tv, p, d, plan.tiles == 2, stream) == 0 ? ATTN_OK : ATTN_ERR_CUDA;
 }

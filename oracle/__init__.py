@@ -11,3 +11,7 @@ from .attention import (  # noqa: F401
     document_ids, gather_paged, head_scores, merge_partials, softcap_scores, softmax_rows, split_bounds,
     tile_map, visible, visible_pairs,
 )
+from .serving import (  # noqa: F401
+    decode_tree, norm, norm_backward, page_tables, qk_norm_rope, qk_norm_rope_backward, rotate,
+    tree_depth, tree_parent,
+)

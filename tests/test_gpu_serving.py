@@ -1,0 +1,640 @@
+"""The operators around the attention kernels on the GPU, against their fp64 definitions.
+
+Tolerances count roundings.  bf16 rounds by at most 2^-8 of the value, fp32 by 2^-24 (u below).
+* Norm and rotation: y = r (z_a c - z_b s) in fp32.  The 128-term sum of squares has 12
+  dependent steps (8 in a lane, 4 shuffles), rsqrt 2, the products and the rotation under 8:
+  at most 32 u of |r z_a c| + |r z_b s|, then one rounding to bf16.
+* Its backward: dx = r (t - x m), two such sums: 40 u of r (|t| + |x| M), M = r^2 mean|x t|;
+  a gain's gradient adds its rows in a chain of fewer than 300 steps: 340 u of the sum of
+  |dz x r|.
+* Tree attention: the weights are rounded to bf16 before the product and O once after:
+  2^-8 (|O| + A) with A = sum_j P_j |V_j|, and 2 % of that for the second order and the fp32
+  steps.  LSE: a score is off by at most (d + 2) u of scale sum_c |q_c k_c|, and the sum of
+  exponentials, its joins, the base-2 logarithm and the exponential by 600 u.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import workloads
+from io_aware_softmax_b200 import (attn_bwd, attn_decode_paged, attn_decode_tree,
+                                   attn_decode_tree_workspace_bytes, attn_fwd, attn_page_tables,
+                                   attn_qk_norm_rope, attn_qk_norm_rope_bwd,
+                                   attn_qk_norm_rope_bwd_workspace_bytes, attn_qk_norm_rope_paged,
+                                   device_status)
+from tests.gpu_common import f64
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+BF = 2.0 ** -8
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def randn(shape, seed, k=0, std=1.0):
+    return workloads.randn_bf16(shape, seed, k, std).cuda()
+
+
+def within(got, want, bound, what):
+    got = f64(got) if isinstance(got, torch.Tensor) else got
+    assert got.shape == want.shape, (what, got.shape, want.shape)
+    bad = ~(np.abs(got - want) <= bound)
+    assert not bad.any(), (what, int(bad.sum()), np.argwhere(bad)[:4].tolist(), got[bad][:4],
+                           want[bad][:4])
+
+
+# ------------------------------------------------------------------------- page tables
+
+def check_tables(ctx, new, pool, table, page, T, used=None, parents=None):
+    got = attn_page_tables(i32(ctx), i32(new), i32(pool), t := i32(table).reshape(len(ctx), -1),
+                           page_size=page, num_tokens=T,
+                           free_used=None if used is None else i32([used]),
+                           parents=None if parents is None else i32(parents))
+    want = oracle.page_tables(ctx, new, pool, np.reshape(table, (len(ctx), -1)), page, T,
+                              used or 0, parents)
+    for g, w, name in zip((*got, t), want,
+                          ("slots", "positions", "seq_lens", "offsets", "used", "table")):
+        assert np.array_equal(g.cpu().numpy(), w), (name, g.cpu().numpy(), w)
+
+
+@pytest.mark.parametrize("page", [1, 3, 16, 64])
+@pytest.mark.parametrize("B", [1, 2, 7, 255, 256, 257, 700])
+def test_page_tables_random(page, B):
+    rng = np.random.default_rng(B * 100 + page)
+    P = 40
+    ctx = rng.integers(-2, P * page + 3, B)
+    new = rng.integers(-1, 3 * page + 2, B)
+    table = rng.integers(0, 1000, (B, P))
+    pool = rng.permutation(20 * B + 5)
+    total = int(np.maximum(new, 0).sum())
+    for T in (total, total + 13, max(total - 5, 0)):
+        check_tables(ctx.tolist(), new.tolist(), pool.tolist(), table.tolist(), page, T)
+
+
+def test_page_tables_edges():
+    check_tables([0], [0], [], [[]], 64, 0)                       # no room at all
+    check_tables([0], [5], [], [[7, 7]], 4, 5)                    # an empty pool
+    check_tables([5, 1], [9, 9], [1, 2, 3], [[0] * 4] * 2, 4, 18, used=2)
+    check_tables([5, 1], [9, 9], [1, 2, 3], [[0] * 4] * 2, 4, 18, used=-4)
+    check_tables([3, 2 ** 31 - 1], [2 ** 31 - 1, 2 ** 31 - 1], [1, 2, 3], [[0] * 4] * 2, 4, 40)
+    check_tables([0] * 16384, [1] * 16384, list(range(16384)), [[-1]] * 16384, 64, 16384)
+    # a page of the pool or of the table that is no page
+    check_tables([4, 0], [4, 3], [-1, 6], [[-1, 0], [0, 0]], 4, 7)
+
+
+def test_page_tables_no_sequences():
+    e = torch.empty(0, dtype=torch.int32, device="cuda")
+    slots, pos, lens, off, used = attn_page_tables(
+        e, e, e, e.reshape(0, 4), page_size=64, num_tokens=5, free_used=i32([3]))
+    assert slots.tolist() == [-1] * 5 and pos.tolist() == [0] * 5
+    assert off.tolist() == [0] and used.tolist() == [3] and lens.numel() == 0
+
+
+@pytest.mark.parametrize("seed", range(3))
+def test_page_tables_trees(seed):
+    rng = np.random.default_rng(seed)
+    new = rng.integers(0, 130, 9)
+    parents = np.concatenate([rng.integers(-1, np.arange(n) + 2) for n in new] + [[0, 0]])
+    ctx = rng.integers(0, 500, 9)
+    check_tables(ctx.tolist(), new.tolist(), list(range(100)), [[0] * 20] * 9, 32,
+                 len(parents), parents=parents.tolist())
+
+
+def test_page_tables_large_offsets():
+    # slots past 2^31: a page number near 2^31 times its size
+    slots, *_ = attn_page_tables(i32([0]), i32([65]), i32([2 ** 31 - 2, 2 ** 30]), i32([[0, 0]]),
+                                 page_size=64, num_tokens=65)
+    assert slots[0].item() == (2 ** 31 - 2) * 64 and slots[64].item() == 2 ** 30 * 64
+
+
+# ----------------------------------------------------------------- norm and rotation
+
+def rope(rows, rot, far=0):
+    a = (np.arange(rows)[:, None] + far) * 10000.0 ** (-np.arange(0, rot, 2) / max(rot, 1))
+    return torch.from_numpy(np.concatenate([np.cos(a), np.sin(a)], 1).astype(np.float32)).cuda()
+
+
+def prep_inputs(tokens, Hq, Hkv, d, rot, norm, seed, rows=600, std=1.0):
+    x = randn((tokens, Hq + 2 * Hkv, d), seed, 0, std)
+    w = (None, None)
+    if norm:
+        w = tuple((1 + 0.3 * randn((d,), seed, k).float()).bfloat16() for k in (1, 2))
+    return x, w, rope(rows, rot) if rot else None
+
+
+def prep_expected(x, w, table, pos, Hq, eps, inter):
+    args = (f64(x), *(None if a is None else f64(a) for a in w),
+            None if table is None else f64(table), pos)
+    want = oracle.qk_norm_rope(*args, Hq, eps, inter)
+    # what the roundings scale with: the same sums over absolute values
+    mag = [np.abs(a) for a in oracle.qk_norm_rope(*args[:3], None, pos, Hq, eps, inter)]
+    if table is not None and table.shape[1]:
+        cs = np.abs(f64(table))
+        for m in mag[:2]:
+            rot = table.shape[1]
+            lo, hi = oracle.serving._pairs(rot, inter)
+            m[..., lo], m[..., hi] = m[..., lo] + m[..., hi], m[..., lo] + m[..., hi]
+    return want, [BF * np.abs(o) + 32 * U * m + 2.0 ** -133 for o, m in zip(want, mag)]
+
+
+def heads_first(t):      # [B, heads, N, d] -> [tokens, heads, d]
+    return t.transpose(1, 2).reshape(-1, t.shape[1], t.shape[3])
+
+
+PREP = [  # B, N, Hq, Hkv, d, rot, norm, interleaved
+    (1, 1, 1, 1, 64, 64, True, False), (2, 37, 4, 2, 128, 128, True, False),
+    (2, 37, 4, 2, 128, 128, True, True), (3, 65, 5, 1, 64, 32, True, False),
+    (3, 65, 5, 1, 64, 32, True, True), (1, 130, 6, 3, 128, 16, False, True),
+    (1, 130, 6, 3, 128, 48, False, False), (2, 9, 7, 7, 64, 0, True, False),
+    (1, 300, 32, 8, 128, 64, True, False), (2, 5, 3, 2, 64, 64, False, False)]
+
+
+@pytest.mark.parametrize("case", PREP)
+@pytest.mark.parametrize("given", [False, True])
+def test_qk_norm_rope(case, given):
+    B, N, Hq, Hkv, d, rot, norm, inter = case
+    x, w, table = prep_inputs(B * N, Hq, Hkv, d, rot, norm, N + d)
+    rng = np.random.default_rng(N)
+    pos = rng.integers(-3, 603, B * N) if given else np.tile(np.arange(N), B)
+    q, k, v = attn_qk_norm_rope(x.view(B, N, -1, d), *w, table, num_q_heads=Hq, eps=1e-5,
+                                positions=i32(pos).view(B, N) if given else None,
+                                interleaved=inter)
+    assert q.shape == (B, Hq, N, d) and k.shape == v.shape == (B, Hkv, N, d)
+    want, bound = prep_expected(x, w, table, pos, Hq, 1e-5, inter)
+    for got, o, e, name in zip((q, k, v), want, bound, "qkv"):
+        within(heads_first(got), o, e, name)
+    assert torch.equal(heads_first(v), x[:, Hq + Hkv:])
+    assert device_status() == 0
+
+
+def test_qk_norm_rope_values_of_every_size():
+    # rows of zeros, tiny and large values; an infinity stays in its row
+    x, w, table = prep_inputs(6, 2, 1, 128, 128, True, 5)
+    x[0] = 0
+    x[1] *= 2.0 ** -60
+    x[2] *= 2.0 ** 40
+    x[3, 0, 7] = float("inf")
+    q, k, v = attn_qk_norm_rope(x.view(1, 6, 4, 128), *w, table, num_q_heads=2, eps=1e-6)
+    ok = np.array([0, 1, 2, 4, 5])
+    want, bound = prep_expected(x[ok], w, table, ok, 2, 1e-6, False)
+    for got, o, e in zip((q, k, v), want, bound):
+        within(heads_first(got)[ok], o, e, "sizes")
+    assert not q[0, 0, 3].isfinite().all() and q[0, 1, 3].isfinite().all()
+
+
+@pytest.mark.parametrize("case", PREP)
+@pytest.mark.parametrize("given", [False, True])
+def test_qk_norm_rope_bwd(case, given):
+    B, N, Hq, Hkv, d, rot, norm, inter = case
+    x, w, table = prep_inputs(B * N, Hq, Hkv, d, rot, norm, N + d + 1)
+    rng = np.random.default_rng(N)
+    pos = rng.integers(-3, 603, B * N) if given else np.tile(np.arange(N), B)
+    g = [randn((B, h, N, d), 77, i) for i, h in enumerate((Hq, Hkv, Hkv))]
+    dx, dwq, dwk = attn_qk_norm_rope_bwd(x.view(B, N, -1, d), *w, table, *g, eps=1e-5,
+                                         positions=i32(pos).view(B, N) if given else None,
+                                         interleaved=inter)
+    gh = [f64(heads_first(t)) for t in g]
+    wf = [None if a is None else f64(a) for a in w]
+    tf = None if table is None else f64(table)
+    want, wq, wk = oracle.qk_norm_rope_backward(f64(x), *wf, tf, pos, *gh, 1e-5, inter)
+    mags, sums = [], []
+    for lo, hi, wt, gg in ((0, Hq, wf[0], gh[0]), (Hq, Hq + Hkv, wf[1], gh[1])):
+        m = np.abs(gg)
+        if rot:
+            a, b = oracle.serving._pairs(rot, inter)
+            m[..., a], m[..., b] = m[..., a] + m[..., b], m[..., a] + m[..., b]
+        if norm:
+            xs = np.abs(f64(x)[:, lo:hi])
+            r = 1 / np.sqrt((xs * xs).mean(-1, keepdims=True) + 1e-5)
+            t = m * np.abs(wt)
+            sums.append((m * xs * r).sum((0, 1)))
+            m = r * (t + xs * r * r * (xs * t).mean(-1, keepdims=True))
+        mags.append(m)
+    mag = np.concatenate([*mags, np.zeros_like(gh[2])], 1)
+    within(dx.reshape(want.shape), want, BF * np.abs(want) + 40 * U * mag + 2.0 ** -133, "dqkv")
+    if norm:
+        within(dwq, wq, 340 * U * sums[0], "dq_weight")
+        within(dwk, wk, 340 * U * sums[1], "dk_weight")
+    else:
+        assert dwq is None and dwk is None
+    assert device_status() == 0
+
+
+def test_qk_norm_rope_bwd_against_differences_and_the_same_twice():
+    # the kernels' own forward, differenced in the direction of a large step in one value
+    B, N, Hq, Hkv, d = 1, 40, 4, 2, 64
+    x, w, table = prep_inputs(B * N, Hq, Hkv, d, 64, True, 9)
+    x = x.view(B, N, -1, d)
+    g = [randn((B, h, N, d), 78, i) for i, h in enumerate((Hq, Hkv, Hkv))]
+    dx, dwq, dwk = attn_qk_norm_rope_bwd(x, *w, table, *g, eps=1e-5)
+    again = attn_qk_norm_rope_bwd(x, *w, table, *g, eps=1e-5)
+    assert torch.equal(dx, again[0]) and torch.equal(dwq, again[1]) and torch.equal(dwk, again[2])
+
+    def loss(wq):
+        out = attn_qk_norm_rope(x, wq, w[1], table, num_q_heads=Hq, eps=1e-5)
+        return sum((f64(o) * f64(gg)).sum() for o, gg in zip(out, g))
+
+    h = 2.0                       # the result is linear in a gain: only roundings remain
+    for c in (0, 13, 63):
+        up, down = w[0].clone(), w[0].clone()
+        up[c], down[c] = w[0][c] + h, w[0][c] - h
+        step = (up[c] - down[c]).item()
+        diff = (loss(up) - loss(down)) / step
+        # the outputs that move (this value and its partner): each rounded twice by 2^-8 of
+        # about 4, times its gradient, independently over 2 N Hq values
+        assert abs(diff - dwq[c].item()) <= 6 * BF * 4 * np.sqrt(2 * 2 * N * Hq) / step * 2
+        assert abs(dwq[c].item()) > 0
+
+
+def test_qk_norm_rope_bwd_many_blocks():
+    # more rows than one wave of blocks takes: shares of many blocks and trips per warp
+    B, N, Hq, Hkv, d = 2, 3000 + 5, 8, 2, 128
+    x, w, table = prep_inputs(B * N, Hq, Hkv, d, 128, True, 21, rows=N)
+    g = [randn((B, h, N, d), 79, i) for i, h in enumerate((Hq, Hkv, Hkv))]
+    dx, dwq, dwk = attn_qk_norm_rope_bwd(x.view(B, N, -1, d), *w, table, *g)
+    gh = [f64(heads_first(t)) for t in g]
+    want, wq, wk = oracle.qk_norm_rope_backward(f64(x), f64(w[0]), f64(w[1]), f64(table),
+                                                np.tile(np.arange(N), B), *gh, 1e-6)
+    err = np.abs(f64(dx).reshape(want.shape) - want)
+    assert np.linalg.norm(err) <= BF * np.linalg.norm(want)
+    # chain of a thread's own rows, then at most 300 more steps; |dz x r| averages below 1.1
+    for got, ref, h in ((dwq, wq, Hq), (dwk, wk, Hkv)):
+        within(got, ref, 400 * U * 1.1 * B * N * h * np.ones(d), "gain")
+
+
+PAGED = [(1, 1, 1, 64, 64, 64, True, False), (16, 32, 8, 128, 64, 128, True, False),
+         (77, 6, 2, 64, 128, 32, True, True), (40, 7, 1, 128, 192, 16, False, False),
+         (33, 4, 4, 64, 1, 64, False, True), (129, 8, 2, 128, 5, 128, True, False)]
+
+
+@pytest.mark.parametrize("case", PAGED)
+def test_qk_norm_rope_paged(case):
+    T, Hq, Hkv, d, page, rot, norm, inter = case
+    x, w, table = prep_inputs(T, Hq, Hkv, d, rot, norm, T + d)
+    pages = -(-T // page) + 2
+    rng = np.random.default_rng(T)
+    slots = rng.permutation(pages * page)[:T].astype(np.int64)
+    if T > 4:
+        slots[1], slots[3], slots[4] = -1, pages * page, 2 ** 40
+    pos = rng.integers(0, 600, T)
+    kp, vp = (randn((pages, Hkv, page, d), 31, i) for i in range(2))
+    k0, v0 = kp.clone(), vp.clone()
+    q = attn_qk_norm_rope_paged(x, *w, table, i32(pos), torch.from_numpy(slots).cuda(), kp, vp,
+                                eps=1e-5, interleaved=inter)
+    want, bound = prep_expected(x, w, table, pos, Hq, 1e-5, inter)
+    within(q, want[0], bound[0], "q")
+    here = (slots >= 0) & (slots < pages * page)
+    at = slots[here]
+    touched = torch.zeros((pages, page), dtype=torch.bool)
+    touched[at // page, at % page] = True
+    for got, before, i in ((kp, k0, 1), (vp, v0, 2)):
+        rows = got.cpu()[at // page, :, at % page]
+        within(rows, want[i][here], bound[i][here], "kv"[i - 1])
+        keep = ~touched[:, None, :, None].expand(got.shape)
+        assert torch.equal(got.cpu()[keep], before.cpu()[keep])
+    assert device_status() == 0
+
+
+def test_prepared_inputs_train_through_attention():
+    # projection output -> norm and rotation -> attention -> back to the projection's gradient:
+    # the gradient is the directional derivative of the same chain in fp64
+    B, N, Hq, Hkv, d = 1, 96, 4, 2, 64
+    x, w, table = prep_inputs(B * N, Hq, Hkv, d, 64, True, 50, rows=N)
+    x = x.view(B, N, -1, d)
+    q, k, v = attn_qk_norm_rope(x, *w, table, num_q_heads=Hq)
+    o, lse = attn_fwd(q, k, v, mask="causal")
+    do = randn((B, Hq, N, d), 51)
+    dq, dk, dv = attn_bwd(q, k, v, o, lse, do, mask="causal")
+    dx, dwq, dwk = attn_qk_norm_rope_bwd(x, *w, table, dq, dk, dv)
+    assert device_status() == 0
+    pos = np.arange(N)
+    xs = f64(x).reshape(N, -1, d)
+    qq, kk, vv = oracle.qk_norm_rope(xs, f64(w[0]), f64(w[1]), f64(table), pos, Hq, 1e-6)
+    swap = lambda a: a.transpose(1, 0, 2)[None]  # noqa: E731
+    g = oracle.attention_backward(swap(qq), swap(kk), swap(vv), f64(do), mask_kind=1)
+    back = [a[0].transpose(1, 0, 2) for a in g]
+    want, wq, wk = oracle.qk_norm_rope_backward(xs, f64(w[0]), f64(w[1]), f64(table), pos, *back,
+                                                1e-6)
+    # attn_bwd's own bounds (1.5e-2 of the largest, 4e-3 of the mean) and the roundings here
+    err = np.abs(f64(dx).reshape(want.shape) - want)
+    assert err.max() <= 1.5e-2 * np.abs(want).max() + BF * np.abs(want).max()
+    assert err.mean() <= (4e-3 + BF) * np.abs(want).mean()
+    for got, ref in ((dwq, wq), (dwk, wk)):
+        assert np.abs(f64(got) - ref).max() <= 1.5e-2 * np.abs(ref).max()
+
+
+# --------------------------------------------------------------------- tree attention
+
+def tree_inputs(lens, n, Hq, Hkv, d, page, seed, std=1.0, spare_rows=0, branch=4):
+    rng = np.random.default_rng(seed)
+    T = sum(n) + spare_rows
+    held = [-(-max(L, 0) // page) for L in lens]
+    P = max(max(held), 1)
+    pages = sum(held) + 2
+    q = randn((T, Hq, d), seed, 0, std)
+    kp = randn((pages, Hkv, page, d), seed, 1, std)
+    vp = randn((pages, Hkv, page, d), seed, 2)
+    order = rng.permutation(pages)
+    table = np.full((len(lens), P), 2 ** 30, np.int32)
+    at = 0
+    for b, h in enumerate(held):
+        table[b, :h] = order[at:at + h]
+        at += h
+    parents = [max(-1, i - 1 - int(rng.integers(branch))) for m in n for i in range(m)]
+    offsets = np.concatenate([[0], np.cumsum(n)])
+    return q, kp, vp, table, offsets, np.array(parents + [0] * spare_rows)
+
+
+def check_tree(lens, n, Hq, Hkv, d, page, seed, chain=False, std=1.0, max_nodes=None, scale=None,
+               parents=None, **kw):
+    q, kp, vp, table, offsets, par = tree_inputs(lens, n, Hq, Hkv, d, page, seed, std)
+    par = None if chain else par if parents is None else np.array(parents)
+    nodes = max(n) if max_nodes is None else max_nodes
+    out = torch.full_like(q, 7.0)
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    attn_decode_tree(q, kp, vp, i32(table), i32(lens), i32(offsets), max_nodes=nodes, scale=scale,
+                     parents=None if chain else i32(par), out=out, lse=lse, **kw)
+    assert device_status() == 0
+    O, L, A = oracle.decode_tree(f64(q), f64(kp), f64(vp), table, lens, offsets, par, scale, nodes)
+    mine = ~np.isnan(L)
+    within(f64(out)[mine], O[mine], 1.02 * BF * (np.abs(O) + A)[mine] + 2.0 ** -133, "O")
+    got = f64(lse)
+    none = np.isneginf(L)
+    assert np.array_equal(np.isneginf(got), none)
+    length = lambda x: np.linalg.norm(f64(x), axis=-1).max(initial=0)  # noqa: E731
+    s = (scale or d ** -0.5) * length(q) * length(kp)
+    some = mine & ~none
+    within(got[some], L[some], U * ((d + 2) * s + 600 + np.abs(L[some])), "LSE")
+    assert (f64(out)[~mine] == 7).all() and (got[~mine] == 7).all()
+    return out, lse
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [64, 128, 192])
+def test_tree_lengths(d, page):
+    n = [1, 2, 5, 8, 3, 7, 1, 8, 4]
+    lens = [1, 2, 63, 64, 65, 128, 129, 700, 1025]
+    check_tree(lens, n, 8, 2, d, page, seed=d + page)
+    check_tree(lens, n, 8, 2, d, page, seed=d + page + 1, chain=True)
+
+
+@pytest.mark.parametrize("G,nodes", [(1, 1), (1, 128), (2, 65), (3, 43), (3, 40), (4, 32), (4, 33),
+                                     (4, 64), (5, 26), (7, 19), (8, 16), (8, 17), (16, 8), (16, 9),
+                                     (16, 40), (12, 128)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_tree_group_sizes_and_widths(G, nodes, d):
+    n = [nodes, max(1, nodes // 3), nodes - 1, 1]
+    check_tree([m + c for m, c in zip(n, (300, 0, 517, 40))], n, 2 * G, 2, d, 64, seed=G * nodes)
+
+
+def test_tree_nodes_across_a_tile_and_a_page():
+    # drafted rows that begin in one 128-key tile and end in the next, at every offset near it
+    for ctx in (60, 100, 120, 126, 127, 128, 129, 250):
+        check_tree([ctx + 90, ctx + 128], [90, 128], 2, 1, 64, 64, seed=ctx)
+
+
+def test_tree_empty_sequences_short_lengths_and_rows_left_alone():
+    check_tree([100, 0, 300, 50, 0], [4, 0, 0, 3, 0], 4, 2, 128, 64, seed=1)
+    # lengths below the number of drafted tokens, zero and negative
+    check_tree([3, 0, -7, 200], [5, 4, 2, 6], 4, 2, 128, 64, seed=2)
+    # only the first max_nodes of a longer sequence
+    check_tree([90, 200], [30, 9], 4, 2, 64, 64, seed=3, max_nodes=7)
+    check_tree([190, 200], [100, 9], 4, 2, 64, 64, seed=4, max_nodes=70)
+    check_tree([1000], [200], 2, 2, 64, 64, seed=5, max_nodes=128)
+    # nothing drafted at all
+    check_tree([100, 30], [0, 0], 4, 2, 64, 64, seed=6, max_nodes=4)
+
+
+def test_tree_bad_parents_count_as_none():
+    check_tree([80], [8], 4, 2, 64, 64, seed=7, parents=[5, 1, 0, -9, 2, 900, 4, 7])
+    deep = list(range(-1, 127))
+    check_tree([700], [128], 1, 1, 128, 64, seed=8, parents=deep)
+
+
+def test_tree_large_scores_and_scale():
+    check_tree([900, 333], [9, 12], 8, 2, 128, 64, seed=9, std=3.0)
+    check_tree([900, 333], [9, 12], 8, 2, 64, 64, seed=10, scale=0.5)
+
+
+def test_tree_many_short_sequences():
+    rng = np.random.default_rng(11)
+    n = rng.integers(0, 6, 500).tolist()
+    lens = [m + int(c) for m, c in zip(n, rng.integers(0, 300, 500))]
+    check_tree(lens, n, 4, 2, 64, 64, seed=11)
+
+
+def test_tree_one_long_sequence_over_many_ctas():
+    check_tree([20011], [11], 4, 1, 128, 64, seed=12)
+    check_tree([20011, 5], [70, 5], 4, 1, 128, 128, seed=13)
+
+
+def test_tree_rows_behind_the_last_sequence_and_garbage_past_the_end():
+    # rows of q past the last offset stay; what pages hold past a sequence's end may be anything
+    q, kp, vp, table, offsets, par = tree_inputs([70, 150], [5, 9], 8, 2, 128, 64, 14, spare_rows=6)
+    O, L, A = oracle.decode_tree(f64(q), f64(kp), f64(vp), table, [70, 150], offsets, par)
+    for p in (kp, vp):
+        p[int(table[0, 1]), :, 6:] = float("nan")
+        p[int(table[1, 2]), :, 22:] = float("inf")
+    out, lse = torch.full_like(q, 3.0), torch.full(q.shape[:2], 3.0, device="cuda")
+    attn_decode_tree(q, kp, vp, i32(table), i32([70, 150]), i32(offsets), max_nodes=9,
+                     parents=i32(par), out=out, lse=lse)
+    assert device_status() == 0
+    within(f64(out)[:14], O[:14], 1.02 * BF * (np.abs(O) + A)[:14], "O")
+    assert (out[14:] == 3).all() and (lse[14:] == 3).all() and lse[:14].isfinite().all()
+
+
+def test_tree_garbage_past_the_end_of_long_sequences():
+    # the last tile comes many rounds of the tile ring after the first
+    lens, n = [3000, 1777, 2600], [6, 3, 1]
+    q, kp, vp, table, offsets, par = tree_inputs(lens, n, 4, 1, 128, 64, 17)
+    O, L, A = oracle.decode_tree(f64(q), f64(kp), f64(vp), table, lens, offsets, par)
+    for b, length in enumerate(lens):
+        for p in (kp, vp):
+            p[int(table[b, length // 64]), :, length % 64:] = float("nan")
+    out, lse = attn_decode_tree(q, kp, vp, i32(table), i32(lens), i32(offsets), max_nodes=6,
+                                parents=i32(par))
+    assert device_status() == 0
+    within(out, O, 1.02 * BF * (np.abs(O) + A), "O")
+    assert np.abs(f64(lse) - L).max() <= 1e-4
+
+
+def test_tree_pages_outside_the_cache_read_zeros():
+    q, kp, vp, table, offsets, par = tree_inputs([200, 100], [3, 4], 4, 2, 64, 64, 15)
+    table[0, 1], table[1, 0] = -1, kp.shape[0]
+    out, lse = attn_decode_tree(q, kp, vp, i32(table), i32([200, 100]), i32(offsets), max_nodes=4,
+                                parents=i32(par))
+    assert device_status() == 0
+    O, L, A = oracle.decode_tree(f64(q), f64(kp), f64(vp), table, [200, 100], offsets, par)
+    within(out, O, 1.02 * BF * (np.abs(O) + A), "O")
+    assert np.abs(f64(lse) - L).max() <= 1e-4
+    # a cache without a page
+    out, lse = attn_decode_tree(q, kp[:0], vp[:0], i32(table), i32([200, 100]), i32(offsets),
+                                max_nodes=4)
+    assert device_status() == 0 and not out.any() and lse.isneginf().all()
+
+
+def test_tree_of_one_node_is_the_paged_decode():
+    q, kp, vp, table, offsets, _ = tree_inputs([900, 64, 1], [1, 1, 1], 8, 2, 128, 64, 16)
+    o1, l1 = attn_decode_tree(q, kp, vp, i32(table), i32([900, 64, 1]), i32(offsets), max_nodes=1)
+    o2, l2 = attn_decode_paged(q.unsqueeze(2), kp, vp, i32(table), i32([900, 64, 1]))
+    assert device_status() == 0
+    # the two kernels round the weights alike but at other maxima
+    assert (o1 - o2.squeeze(2)).abs().max().item() <= 2e-2
+    assert (l1 - l2.squeeze(2)).abs().max().item() <= 1e-4
+
+
+# ------------------------------------------------------------------- a step of serving
+
+def _step(s, o):
+    """One verification step on preallocated buffers: tables, cache write, attention."""
+    attn_page_tables(s["ctx"], s["new"], s["free"], s["table"], page_size=64,
+                     num_tokens=s["qkv"].shape[0], parents=s["parents"], free_used=s["used"],
+                     slots=o["slots"], positions=o["pos"], seq_lens=o["lens"],
+                     token_offsets=o["off"], pages_used=o["used"])
+    attn_qk_norm_rope_paged(s["qkv"], s["wq"], s["wk"], s["rope"], o["pos"], o["slots"], s["k"],
+                            s["v"], q=o["q"])
+    attn_decode_tree(o["q"], s["k"], s["v"], s["table"], o["lens"], o["off"], max_nodes=9,
+                     parents=s["parents"], out=o["out"], lse=o["lse"], workspace=o["ws"])
+
+
+def _step_state(seed):
+    rng = np.random.default_rng(seed)
+    ctx, new = rng.integers(0, 400, 5), rng.integers(1, 10, 5)
+    ctx[2] = 0
+    T, Hq, Hkv, d = 48, 4, 2, 64
+    pool = rng.permutation(60)
+    table = np.full((5, 8), -1)
+    used = 3
+    for b in range(5):
+        for p in range(-(-int(ctx[b]) // 64)):
+            table[b, p] = pool[used]
+            used += 1
+    parents = [max(-1, i - 1 - int(rng.integers(3))) for m in new for i in range(m)]
+    parents += [-1] * (T - len(parents))
+    x, w, rp = prep_inputs(T, Hq, Hkv, d, 64, True, seed)
+    return dict(ctx=i32(ctx), new=i32(new), free=i32(pool), table=i32(table), used=i32([used]),
+                parents=i32(parents), qkv=x, wq=w[0], wk=w[1], rope=rp,
+                k=randn((60, Hkv, 64, d), seed, 5), v=randn((60, Hkv, 64, d), seed, 6))
+
+
+def _step_outputs():
+    e = lambda shape, t: torch.zeros(shape, dtype=t, device="cuda")  # noqa: E731
+    return dict(slots=e(48, torch.int64), pos=e(48, torch.int32), lens=e(5, torch.int32),
+                off=e(6, torch.int32), used=e(1, torch.int32), q=e((48, 4, 64), torch.bfloat16),
+                out=e((48, 4, 64), torch.bfloat16), lse=e((48, 4), torch.float32),
+                ws=e(attn_decode_tree_workspace_bytes(5, 4, 2, 9, 64), torch.uint8))
+
+
+def test_a_verification_step_against_the_definitions():
+    s, o = _step_state(60), _step_outputs()
+    k0, v0 = f64(s["k"]), f64(s["v"])
+    ctx, new, par = (s[n].tolist() for n in ("ctx", "new", "parents"))
+    want = oracle.page_tables(ctx, new, s["free"].tolist(), s["table"].cpu().numpy(), 64, 48,
+                              s["used"].item(), par)
+    _step(s, o)
+    assert device_status() == 0
+    for n, w in zip(("slots", "pos", "lens", "off", "used"), want):
+        assert np.array_equal(o[n].cpu().numpy(), w), n
+    assert np.array_equal(s["table"].cpu().numpy(), want[5])
+    slots, pos = want[0], want[1]
+    heads, bound = prep_expected(s["qkv"], (s["wq"], s["wk"]), s["rope"], pos, 4, 1e-6, False)
+    within(o["q"], heads[0], bound[0], "q")
+    for page, before, x, e in ((s["k"], k0, heads[1], bound[1]), (s["v"], v0, heads[2], bound[2])):
+        t = np.nonzero(slots >= 0)[0]
+        within(f64(page)[slots[t] // 64, :, slots[t] % 64], x[t], e[t], "cache")
+    # the attention of what was written
+    O, L, A = oracle.decode_tree(f64(o["q"]), f64(s["k"]), f64(s["v"]), want[5], want[2], want[3],
+                                 par)
+    T = want[3][-1]
+    within(f64(o["out"])[:T], O[:T], 1.02 * BF * (np.abs(O) + A)[:T] + 2.0 ** -133, "O")
+    assert np.abs(f64(o["lse"])[:T] - L[:T]).max() <= 1e-4
+    assert not o["out"][T:].any()
+
+
+def test_the_step_captured_and_replayed():
+    s, eager, cap = _step_state(61), _step_outputs(), _step_outputs()
+    _step(s, eager)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _step(s, cap)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _step(s, cap)
+    for seed in (61, 62, 63):          # lengths, tables and trees of other steps, in place
+        new = _step_state(seed)
+        for n in s:
+            s[n].copy_(new[n])
+        fresh = _step_outputs()
+        _step(new, fresh)
+        for n in ("out", "lse", "q"):
+            cap[n].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert device_status() == 0
+        for n in fresh:
+            if n != "ws":
+                assert torch.equal(cap[n], fresh[n]), n
+        assert torch.equal(s["k"], new["k"]) and torch.equal(s["table"], new["table"])
+
+
+def test_backward_captured_and_replayed():
+    B, N, Hq, Hkv, d = 2, 70, 4, 2, 128
+    x, w, table = prep_inputs(B * N, Hq, Hkv, d, 128, True, 70, rows=N)
+    x = x.view(B, N, -1, d)
+    g = [randn((B, h, N, d), 71, i) for i, h in enumerate((Hq, Hkv, Hkv))]
+    out = dict(dqkv=torch.empty_like(x), dq_weight=torch.empty(d, device="cuda"),
+               dk_weight=torch.empty(d, device="cuda"),
+               workspace=torch.empty(attn_qk_norm_rope_bwd_workspace_bytes(d), dtype=torch.uint8,
+                                     device="cuda"))
+    want = attn_qk_norm_rope_bwd(x, *w, table, *g)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        attn_qk_norm_rope_bwd(x, *w, table, *g, **out)
+    graph.replay()
+    for a, b in zip(want, (out["dqkv"], out["dq_weight"], out["dk_weight"])):
+        assert torch.equal(a, b)
+
+
+def test_two_streams_at_once():
+    states = [_step_state(80 + i) for i in range(2)]
+    want = []
+    for s in states:
+        fresh = {n: t.clone() for n, t in s.items()}
+        o = _step_outputs()
+        _step(fresh, o)
+        want.append(o)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in states]
+    got = [_step_outputs() for _ in states]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, o, st in zip(states, got, streams):
+            with torch.cuda.stream(st):
+                _step(s, o)
+    torch.cuda.synchronize()
+    assert device_status() == 0
+    for a, b in zip(got, want):
+        for n in a:
+            if n != "ws":
+                assert torch.equal(a[n], b[n]), n
+
+
+def test_empty_calls():
+    e = lambda *shape: torch.zeros(shape, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    w = e(64)
+    q, k, v = attn_qk_norm_rope(e(2, 0, 4, 64), w, w, None, num_q_heads=2)
+    assert q.shape == (2, 2, 0, 64)
+    g = attn_qk_norm_rope_bwd(e(2, 0, 4, 64), w, w, None, q, k, v,
+                              dq_weight=torch.ones(64, device="cuda"))
+    assert not g[1].any() and not g[2].any()
+    kp = e(1, 1, 64, 64)
+    q = attn_qk_norm_rope_paged(e(0, 4, 64), w, w, None, i32([]), i32([]).long(), kp, kp.clone())
+    o, lse = attn_decode_tree(q, kp, kp, i32([[0]]), i32([5]), i32([0, 0]), max_nodes=4)
+    assert o.shape == (0, 2, 64) and lse.shape == (0, 2)
+    assert device_status() == 0
