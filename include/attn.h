@@ -341,9 +341,9 @@ ATTN_API int attn_page_tables(const int* ctx_lens, const int* new_lens, const in
  *   positions   int32 [B, N], or NULL: row n has position n.  A position outside
  *            [0, table_rows) reads a table row of zeros.
  *   interleaved 0: pair i is (i, i + rot / 2); else (2 i, 2 i + 1)
- *   eps      > 0 (with a norm)
+ *   eps      positive and normal in fp32 (with a norm)
  * Statistics and products are fp32, outputs rounded once.
- * Errors: INVALID_ARG, UNSUPPORTED (d; rot), MISALIGNED, CUDA.
+ * Errors: INVALID_ARG, UNSUPPORTED (d; rot; more than 4096 heads), MISALIGNED, CUDA.
  */
 ATTN_API int attn_qk_norm_rope(const void* qkv, const void* q_weight, const void* k_weight,
              const float* rope_table, const int* positions, void* q, void* k, void* v, int B,

@@ -79,6 +79,8 @@ class LibraryMissing(RuntimeError):
 def load(path: str = LIB_PATH):
     """Loads the library once and attaches the signatures; raises LibraryMissing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -4,6 +4,7 @@ in the library's CUDA kernels; nothing here computes attention.
 """
 from __future__ import annotations
 
+import contextlib
 from typing import Optional, Tuple
 
 import torch
@@ -40,7 +41,9 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 def _stream(device: torch.device, stream=None) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        # the handle of torch.cuda.current_stream(device), without building a Stream object
+        return torch._C._cuda_getCurrentRawStream(
+            device.index if device.index is not None else torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -102,8 +105,13 @@ def _index(t: torch.Tensor) -> int:
     return t.device.index if t.device.index is not None else torch.cuda.current_device()
 
 
+_CURRENT = contextlib.nullcontext()
+
+
 def _device(t: torch.Tensor):
     """Makes t's device current for the call: the library launches on the current device."""
+    if torch.cuda.current_device() == t.device.index:
+        return _CURRENT
     return torch.cuda.device(t.device)
 
 
@@ -426,12 +434,25 @@ def attn_merge(o_part: torch.Tensor, lse_part: torch.Tensor, *, out: Optional[to
     return out, lse
 
 
-def _int32(t: Optional[torch.Tensor], name: str, shape, ref: torch.Tensor):
-    """Checks an optional int32 array (lengths, tables, indices)."""
+def _given(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, ref: torch.Tensor):
+    """One tensor of a call: dtype, exact shape, contiguous, on ref's device (which the caller
+    has checked).  One pass over the properties; only a mismatch looks for which it is."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.device == ref.device and t.is_contiguous()):
+        _out(t, name, dtype, shape, ref)
+
+
+def _optional(t, name: str, dtype: torch.dtype, shape, ref: torch.Tensor):
     if t is not None:
-        _need(t, name, torch.int32, len(shape))
-        _shape(t, name, shape)
-        _same_device(ref, (t, name))
+        _given(t, name, dtype, shape, ref)
+
+
+def _result(t, name: str, dtype: torch.dtype, shape, ref: torch.Tensor) -> torch.Tensor:
+    """A caller-supplied output, checked, or a new one."""
+    if t is None:
+        return ref.new_empty(shape, dtype=dtype)
+    _given(t, name, dtype, shape, ref)
+    return t
 
 
 def attn_page_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor,
@@ -451,37 +472,30 @@ def attn_page_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages:
     the tokens of drafted trees positions by depth; ``free_used`` is the pages_used of an
     earlier step on the same free list."""
     lib = _lib.load()
-    _need(ctx_lens, "ctx_lens", torch.int32, 1)
-    _need(free_pages, "free_pages", torch.int32, 1)
-    _need(block_table, "block_table", torch.int32, 2)
-    B, max_pages = ctx_lens.shape[0], block_table.shape[1]
-    T, dev = int(num_tokens), ctx_lens.device
+    i32 = torch.int32
+    _need(ctx_lens, "ctx_lens", i32, 1)
+    _need(free_pages, "free_pages", i32, 1)
+    _need(block_table, "block_table", i32, 2)
+    B, max_pages, T = ctx_lens.shape[0], block_table.shape[1], int(num_tokens)
     if T < 0:
         raise ValueError("num_tokens must not be negative")
     if block_table.shape[0] != B:
         raise ValueError("block_table needs one row per sequence")
     _same_device(ctx_lens, (free_pages, "free_pages"), (block_table, "block_table"))
-    _int32(new_lens, "new_lens", (B,), ctx_lens)
-    _int32(free_used, "free_used", (1,), ctx_lens)
-    _int32(parents, "parents", (T,), ctx_lens)
-
-    def output(t, name, dtype, shape):
-        if t is None:
-            return torch.empty(shape, dtype=dtype, device=dev)
-        _out(t, name, dtype, shape, ctx_lens)
-        return t
-
-    slots = output(slots, "slots", torch.int64, (T,))
-    positions = output(positions, "positions", torch.int32, (T,))
-    seq_lens = output(seq_lens, "seq_lens", torch.int32, (B,))
-    token_offsets = output(token_offsets, "token_offsets", torch.int32, (B + 1,))
-    pages_used = output(pages_used, "pages_used", torch.int32, (1,))
+    _given(new_lens, "new_lens", i32, (B,), ctx_lens)
+    _optional(free_used, "free_used", i32, (1,), ctx_lens)
+    _optional(parents, "parents", i32, (T,), ctx_lens)
+    slots = _result(slots, "slots", torch.int64, (T,), ctx_lens)
+    positions = _result(positions, "positions", i32, (T,), ctx_lens)
+    seq_lens = _result(seq_lens, "seq_lens", i32, (B,), ctx_lens)
+    token_offsets = _result(token_offsets, "token_offsets", i32, (B + 1,), ctx_lens)
+    pages_used = _result(pages_used, "pages_used", i32, (1,), ctx_lens)
     with _device(ctx_lens):
         st = lib.attn_page_tables(_ptr(ctx_lens), _ptr(new_lens), _ptr(free_pages),
                                   _ptr(free_used), _ptr(parents), _ptr(block_table), _ptr(slots),
                                   _ptr(positions), _ptr(seq_lens), _ptr(token_offsets),
                                   _ptr(pages_used), B, max_pages, int(page_size),
-                                  free_pages.shape[0], T, _stream(dev, stream))
+                                  free_pages.shape[0], T, _stream(ctx_lens.device, stream))
     _check(st, "attn_page_tables")
     return slots, positions, seq_lens, token_offsets, pages_used
 
@@ -489,19 +503,18 @@ def attn_page_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages:
 def _prep_inputs(qkv: torch.Tensor, dims: int, q_weight, k_weight, rope_table):
     """Checks the projection's output, the gains and the angle table; returns (rot, rows)."""
     _need(qkv, "qkv", torch.bfloat16, dims)
-    d = qkv.shape[-1]
     if (q_weight is None) != (k_weight is None):
         raise ValueError("q_weight and k_weight are given together, or neither")
     if q_weight is not None:
-        for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-            _need(t, n, torch.bfloat16, 1)
-            _shape(t, n, (d,))
-            _same_device(qkv, (t, n))
+        shape = qkv.shape[-1:]
+        _given(q_weight, "q_weight", torch.bfloat16, shape, qkv)
+        _given(k_weight, "k_weight", torch.bfloat16, shape, qkv)
     if rope_table is None:
         return 0, 0
     _need(rope_table, "rope_table", torch.float32, 2)
     _same_device(qkv, (rope_table, "rope_table"))
-    return rope_table.shape[1], rope_table.shape[0]
+    rows, rot = rope_table.shape
+    return rot, rows
 
 
 def attn_qk_norm_rope(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
@@ -523,16 +536,10 @@ def attn_qk_norm_rope(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
     if not 0 < Hq < H or (H - Hq) % 2:
         raise ValueError(f"{H} heads cannot be {Hq} query heads and as many key as value heads")
     Hkv = (H - Hq) // 2
-    _int32(positions, "positions", (B, N), qkv)
-    shapes = ((B, Hq, N, d), (B, Hkv, N, d), (B, Hkv, N, d))
-    out = []
-    for t, n, shape in zip((q, k, v), "qkv", shapes):
-        if t is None:
-            t = torch.empty(shape, dtype=torch.bfloat16, device=qkv.device)
-        else:
-            _out(t, n, torch.bfloat16, shape, qkv)
-        out.append(t)
-    q, k, v = out
+    _optional(positions, "positions", torch.int32, (B, N), qkv)
+    q = _result(q, "q", torch.bfloat16, (B, Hq, N, d), qkv)
+    k = _result(k, "k", torch.bfloat16, (B, Hkv, N, d), qkv)
+    v = _result(v, "v", torch.bfloat16, (B, Hkv, N, d), qkv)
     with _device(qkv):
         st = lib.attn_qk_norm_rope(_ptr(qkv), _ptr(q_weight), _ptr(k_weight), _ptr(rope_table),
                                    _ptr(positions), _ptr(q), _ptr(k), _ptr(v), B, N, Hq, Hkv, d,
@@ -555,38 +562,30 @@ def attn_qk_norm_rope_bwd(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
     lib = _lib.load()
     rot, rows = _prep_inputs(qkv, 4, q_weight, k_weight, rope_table)
     B, N, H, d = qkv.shape
-    for t, n in ((dq, "dq"), (dk, "dk"), (dv, "dv")):
-        _need(t, n, torch.bfloat16, 4)
+    bf16 = torch.bfloat16
+    _need(dq, "dq", bf16, 4)
+    _need(dk, "dk", bf16, 4)
     Hq, Hkv = dq.shape[1], dk.shape[1]
     if Hq + 2 * Hkv != H:
         raise ValueError(f"dq and dk have {Hq} and {Hkv} heads, qkv {H}")
-    _shape(dq, "dq", (B, Hq, N, d))
-    _shape(dk, "dk", (B, Hkv, N, d))
-    _shape(dv, "dv", (B, Hkv, N, d))
-    _same_device(qkv, (dq, "dq"), (dk, "dk"), (dv, "dv"))
-    _int32(positions, "positions", (B, N), qkv)
-    if dqkv is None:
-        dqkv = torch.empty_like(qkv)
-    else:
-        _out(dqkv, "dqkv", torch.bfloat16, qkv.shape, qkv)
+    _given(dq, "dq", bf16, (B, Hq, N, d), qkv)
+    _given(dk, "dk", bf16, (B, Hkv, N, d), qkv)
+    _given(dv, "dv", bf16, (B, Hkv, N, d), qkv)
+    _optional(positions, "positions", torch.int32, (B, N), qkv)
+    dqkv = _result(dqkv, "dqkv", bf16, qkv.shape, qkv)
     ws_bytes = 0
     if q_weight is None:
         if dq_weight is not None or dk_weight is not None:
             raise ValueError("without a norm there are no gains to take gradients of")
         workspace = None
     else:
-        grads = []
-        for t, n in ((dq_weight, "dq_weight"), (dk_weight, "dk_weight")):
-            if t is None:
-                t = torch.empty((d,), dtype=torch.float32, device=qkv.device)
-            else:
-                _out(t, n, torch.float32, (d,), qkv)
-            grads.append(t)
-        dq_weight, dk_weight = grads
+        dq_weight = _result(dq_weight, "dq_weight", torch.float32, (d,), qkv)
+        dk_weight = _result(dk_weight, "dk_weight", torch.float32, (d,), qkv)
         if workspace is None:
-            need = attn_qk_norm_rope_bwd_workspace_bytes(d)
-            workspace = torch.empty(need, dtype=torch.uint8, device=qkv.device)
-        ws_bytes = _workspace(workspace, qkv)
+            ws_bytes = int(lib.attn_qk_norm_rope_bwd_workspace_bytes(d))
+            workspace = qkv.new_empty(ws_bytes, dtype=torch.uint8)
+        else:
+            ws_bytes = _workspace(workspace, qkv)
     with _device(qkv):
         st = lib.attn_qk_norm_rope_bwd(_ptr(qkv), _ptr(q_weight), _ptr(k_weight),
                                        _ptr(rope_table), _ptr(positions), _ptr(dq), _ptr(dk),
@@ -614,24 +613,17 @@ def attn_qk_norm_rope_paged(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
     lib = _lib.load()
     rot, rows = _prep_inputs(qkv, 3, q_weight, k_weight, rope_table)
     T, H, d = qkv.shape
-    _need(k_pages, "k_pages", torch.bfloat16, 4)
-    _need(v_pages, "v_pages", torch.bfloat16, 4)
-    num_pages, Hkv, page_size = k_pages.shape[:3]
-    _shape(k_pages, "k_pages", (num_pages, Hkv, page_size, d))
-    _shape(v_pages, "v_pages", k_pages.shape)
+    bf16 = torch.bfloat16
+    _need(k_pages, "k_pages", bf16, 4)
+    num_pages, Hkv, page_size, _ = k_pages.shape
+    _given(k_pages, "k_pages", bf16, (num_pages, Hkv, page_size, d), qkv)
+    _given(v_pages, "v_pages", bf16, (num_pages, Hkv, page_size, d), qkv)
     Hq = H - 2 * Hkv
     if Hq <= 0:
         raise ValueError(f"qkv has {H} heads: none for queries beside {Hkv} key and value heads")
-    if positions is None:
-        raise TypeError("positions must be a torch.Tensor")
-    _int32(positions, "positions", (T,), qkv)
-    _need(slots, "slots", torch.int64, 1)
-    _shape(slots, "slots", (T,))
-    _same_device(qkv, (k_pages, "k_pages"), (v_pages, "v_pages"), (slots, "slots"))
-    if q is None:
-        q = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=qkv.device)
-    else:
-        _out(q, "q", torch.bfloat16, (T, Hq, d), qkv)
+    _given(positions, "positions", torch.int32, (T,), qkv)
+    _given(slots, "slots", torch.int64, (T,), qkv)
+    q = _result(q, "q", bf16, (T, Hq, d), qkv)
     with _device(qkv):
         st = lib.attn_qk_norm_rope_paged(_ptr(qkv), _ptr(q_weight), _ptr(k_weight),
                                          _ptr(rope_table), _ptr(positions), _ptr(slots), _ptr(q),
@@ -661,42 +653,33 @@ def attn_decode_tree(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
     parents int32 [T]: index within the sequence of the node each token hangs on, -1 for the
     context; None: a chain.  Rows behind token_offsets[B] are left as they were."""
     lib = _lib.load()
-    _need(q, "q", torch.bfloat16, 3)
+    bf16, i32 = torch.bfloat16, torch.int32
+    _need(q, "q", bf16, 3)
+    _need(k_pages, "k_pages", bf16, 4)
+    _need(block_table, "block_table", i32, 2)
     T, Hq, d = q.shape
-    _need(k_pages, "k_pages", torch.bfloat16, 4)
-    _need(v_pages, "v_pages", torch.bfloat16, 4)
-    num_pages, Hkv, page_size = k_pages.shape[:3]
-    if k_pages.shape[3] != d:
-        raise ValueError(f"k_pages {tuple(k_pages.shape)} must have the head size {d} of q")
-    _shape(v_pages, "v_pages", k_pages.shape)
-    _need(seq_lens, "seq_lens", torch.int32, 1)
-    B = seq_lens.shape[0]
-    _need(block_table, "block_table", torch.int32, 2)
-    if block_table.shape[0] != B:
-        raise ValueError("block_table needs one row per sequence")
-    _same_device(q, (k_pages, "k_pages"), (v_pages, "v_pages"), (block_table, "block_table"),
-                 (seq_lens, "seq_lens"))
-    _need(token_offsets, "token_offsets", torch.int32, 1)
-    _int32(token_offsets, "token_offsets", (B + 1,), q)
-    _int32(parents, "parents", (T,), q)
+    num_pages, Hkv, page_size, _ = k_pages.shape
+    B, max_pages = block_table.shape
+    _given(k_pages, "k_pages", bf16, (num_pages, Hkv, page_size, d), q)
+    _given(v_pages, "v_pages", bf16, (num_pages, Hkv, page_size, d), q)
+    _same_device(q, (block_table, "block_table"))
+    _given(seq_lens, "seq_lens", i32, (B,), q)
+    _given(token_offsets, "token_offsets", i32, (B + 1,), q)
+    _optional(parents, "parents", i32, (T,), q)
     if workspace is None:
-        need = attn_decode_tree_workspace_bytes(B, Hq, Hkv, int(max_nodes), d, _index(q))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    ws_bytes = _workspace(workspace, q)
-    if out is None:
-        out = torch.empty_like(q)
+        ws_bytes = int(lib.attn_decode_tree_workspace_bytes(B, Hq, Hkv, int(max_nodes), d,
+                                                            _index(q)))
+        workspace = q.new_empty(max(ws_bytes, 16), dtype=torch.uint8)
     else:
-        _out(out, "out", torch.bfloat16, (T, Hq, d), q)
-    if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
-    else:
-        _out(lse, "lse", torch.float32, (T, Hq), q)
+        ws_bytes = _workspace(workspace, q)
+    out = _result(out, "out", bf16, (T, Hq, d), q)
+    lse = _result(lse, "lse", torch.float32, (T, Hq), q)
     with _device(q):
         st = lib.attn_decode_tree(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table),
                                   _ptr(seq_lens), _ptr(token_offsets), _ptr(parents), _ptr(out),
-                                  _ptr(lse), B, T, Hq, Hkv, num_pages, page_size,
-                                  block_table.shape[1], int(max_nodes), d, float(scale or 0.0),
-                                  _ptr(workspace), ws_bytes, _stream(q.device, stream))
+                                  _ptr(lse), B, T, Hq, Hkv, num_pages, page_size, max_pages,
+                                  int(max_nodes), d, float(scale or 0.0), _ptr(workspace),
+                                  ws_bytes, _stream(q.device, stream))
     _check(st, "attn_decode_tree")
     return out, lse
 

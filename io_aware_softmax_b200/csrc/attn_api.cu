@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <cfloat>
+#include <climits>
 #include <cmath>
 #include <algorithm>
 #include <cstdint>
@@ -653,7 +655,8 @@ extern "C" int attn_page_tables(const int* ctx_lens, const int* new_lens, const 
                                 cudaStream_t stream) {
   if (B < 0 || max_pages_per_seq < 0 || page_size <= 0 || num_free < 0 || num_tokens < 0)
     return ATTN_ERR_INVALID_ARG;
-  if (B > kPagesMaxSeqs || (long long)max_pages_per_seq * page_size > (1LL << 31) - 1)
+  if (B > kPagesMaxSeqs || num_tokens > INT_MAX - 4 ||
+      (long long)max_pages_per_seq * page_size > (1LL << 31) - 1)
     return ATTN_ERR_UNSUPPORTED;
   if (!token_offsets || !pages_used || (num_tokens > 0 && (!slots || !positions)) ||
       (B > 0 && (!ctx_lens || !new_lens || !seq_lens)) ||
@@ -696,10 +699,10 @@ static int check_prep(PrepParams& p, const void* qkv, const void* q_weight, cons
   if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
   if (rot > d || rot % 16 != 0) return ATTN_ERR_UNSUPPORTED;
   if ((q_weight == nullptr) != (k_weight == nullptr)) return ATTN_ERR_INVALID_ARG;
-  if (q_weight != nullptr && !(eps > 0.f && eps <= 3.4e38f)) return ATTN_ERR_INVALID_ARG;
+  if (q_weight != nullptr && !(eps >= FLT_MIN && eps <= FLT_MAX)) return ATTN_ERR_INVALID_ARG;
   const long long H = (long long)Hq + 2LL * Hkv;
   // rows of one call: a warp takes several, and their number is a 32-bit index
-  if (tokens * H > (1LL << 31) - 1 || H > (1 << 20)) return ATTN_ERR_UNSUPPORTED;
+  if (tokens * H > (1LL << 31) - 1 || H > kPrepMaxHeads) return ATTN_ERR_UNSUPPORTED;
   if (tokens > 0 && H > 0) {
     if (qkv == nullptr || (rot > 0 && table_rows > 0 && rope_table == nullptr))
       return ATTN_ERR_INVALID_ARG;
@@ -740,7 +743,7 @@ extern "C" int attn_qk_norm_rope(const void* qkv, const void* q_weight, const vo
   p.q = q;
   p.k = k;
   p.v = v;
-  return launch_qk_prep(p, d, false, stream) == 0 ? ATTN_OK : ATTN_ERR_CUDA;
+  return launch_qk_prep(p, d, false, sm_count(current_device()), stream) == 0 ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 extern "C" int attn_qk_norm_rope_paged(const void* qkv, const void* q_weight,
@@ -767,7 +770,7 @@ extern "C" int attn_qk_norm_rope_paged(const void* qkv, const void* q_weight,
   p.slots = slots;
   p.page_size = page_size;
   p.num_slots = num_pages * page_size;
-  return launch_qk_prep(p, d, true, stream) == 0 ? ATTN_OK : ATTN_ERR_CUDA;
+  return launch_qk_prep(p, d, true, sm_count(current_device()), stream) == 0 ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 extern "C" size_t attn_qk_norm_rope_bwd_workspace_bytes(int d) {

@@ -13,13 +13,20 @@
 // All of it is bound by the bytes: 2 to 3 passes over the rows and some ten operations a
 // value.  16 (d = 128) or 8 (d = 64) lanes hold a row, 16 bytes each, so loads and stores are
 // whole lines, the sums are shuffles, and a pair's other half is in the same lane
-// (interleaved) or a fixed number of lanes away.  A warp takes kSteps * 32 / lanes rows of ONE
-// token: it issues all their loads first, and reads the token's angles once for all of them.
-// Sums, statistics and the rotation are in fp32; each output is rounded once.
+// (interleaved) or a fixed number of lanes away.  A warp takes a chunk of a token's heads of
+// one kind (query, key or value): the angles and the gain are read and multiplied once,
+//   y = r (x A + x_partner B),  A = w cos,  B = +-w_partner sin,
+// and stay in registers for all rows of the chunk.  The rows come through shared memory, into
+// places that every lane fills and reads for itself (cp.async, no barrier): what is in flight
+// then costs no registers, and one row at a time is computed.  Sums, statistics and the
+// rotation are in fp32; each output is rounded once.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "attn_serve.h"
+#include "sm100_ptx.cuh"
 
 namespace attn {
 
@@ -27,8 +34,14 @@ namespace {
 
 constexpr int kPrepThreads = 256;
 constexpr int kPrepWarps = kPrepThreads / 32;
-constexpr int kFwdSteps = 4;
-constexpr int kBwdSteps = 2;
+// Steps of a chunk at most, all in flight at once (a step is a row a lane: 2 or 4 rows a
+// warp).  Measured on a B200: [8, 4096] tokens of 32 + 2 x 32 heads of 128, forward: 8 steps
+// 241 us, 4 steps 267; [4, 4096] of 32 + 2 x 8, backward: 8 steps 101 us, 4 steps 111.
+constexpr int kChunkSteps = 8;
+// Blocks an SM: the forward at 64 registers a thread, the backward at 128 (with 80 it spills,
+// 128 us instead of 101).
+constexpr int kFwdBlocks = 4;
+constexpr int kBwdBlocks = 2;
 
 template <int D>
 struct Row {
@@ -36,31 +49,48 @@ struct Row {
   static constexpr int kRows = 32 / kLanes;      // rows a warp holds at a time
 };
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+// Two values of a packed bf16 pair.
+__device__ __forceinline__ void unpack2(uint32_t u, float& lo, float& hi) {
+  lo = __uint_as_float(u << 16);
+  hi = __uint_as_float(u & 0xffff0000u);
 }
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
+__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
+  unpack2(u.x, x[0], x[1]);
+  unpack2(u.y, x[2], x[3]);
+  unpack2(u.z, x[4], x[5]);
+  unpack2(u.w, x[6], x[7]);
 }
 
 __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                    pack_bf16x2(x[6], x[7]));
 }
 
-__device__ __forceinline__ uint4 load_once(const void* base, size_t elem) {
+// 16 bytes to this lane's place in shared memory, or zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const __nv_bfloat16* src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+__device__ __forceinline__ uint4 read16(uint32_t src) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(reinterpret_cast<const __nv_bfloat16*>(base) + elem));
+               : "r"(src)
+               : "memory");
   return v;
+}
+
+__device__ __forceinline__ uint4 load_gain(const void* w, int e0) {
+  return __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(w) + e0));
 }
 
 __device__ __forceinline__ void store8(void* base, size_t elem, const uint4& v) {
@@ -74,246 +104,368 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// This lane's coefficients: y[i] = z[i] c[i] + z_partner[i] s[i].  A position outside the
-// table reads a row of zeros, as a page outside the cache does.
+// What this lane's values meet in the rotation: the lane of their partners, and the
+// coefficients of y[i] = z[i] c[i] + z_partner[i] s[i].  A position outside the table reads a
+// row of zeros, as a page outside the cache does.
 template <bool kInter>
 struct Angles {
   float c[8], s[8];
   bool rotates;
-  int partner;      // lane that holds the pairs' other halves (halves layout)
+  int partner;
 
-  __device__ __forceinline__ void load(const PrepParams& p, int pos, int e0, int lane) {
+  __device__ __forceinline__ void place(const PrepParams& p, int e0, int lane) {
     const int half = p.rot >> 1;
     rotates = e0 < p.rot;
     partner = lane;
-    if (!rotates) return;
-    const bool valid = (unsigned)pos < (unsigned)p.table_rows;
-    const float* row = p.table + (size_t)(valid ? pos : 0) * p.rot;
+    if (!kInter && rotates) partner = e0 < half ? lane + (half >> 3) : lane - (half >> 3);
+  }
+
+  // back: the coefficients of the inverse rotation (its transpose has the sines' signs turned)
+  template <bool kBack>
+  __device__ __forceinline__ void load(const PrepParams& p, int pos, int e0) {
+    const int half = p.rot >> 1;
+    const bool valid = rotates && (unsigned)pos < (unsigned)p.table_rows;
+    const float* row = p.table + (valid ? (size_t)pos * p.rot : 0);
+    const float other = rotates ? 0.f : 1.f;
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
     if (kInter) {
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+      float4 a = make_float4(other, other, other, other), b = zero;
       if (valid) {
         a = __ldg(reinterpret_cast<const float4*>(row + (e0 >> 1)));
         b = __ldg(reinterpret_cast<const float4*>(row + half + (e0 >> 1)));
       }
-      const float cc[4] = {a.x, a.y, a.z, a.w}, ss[4] = {b.x, b.y, b.z, b.w};
+      c[0] = c[1] = a.x; c[2] = c[3] = a.y; c[4] = c[5] = a.z; c[6] = c[7] = a.w;
+      const float ss[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        c[2 * i] = c[2 * i + 1] = cc[i];
-        s[2 * i] = -ss[i];
-        s[2 * i + 1] = ss[i];
+        s[2 * i] = kBack ? ss[i] : -ss[i];
+        s[2 * i + 1] = kBack ? -ss[i] : ss[i];
       }
     } else {
       const bool low = e0 < half;
       const int j = low ? e0 : e0 - half;
-      partner = low ? lane + (half >> 3) : lane - (half >> 3);
 #pragma unroll
       for (int i = 0; i < 8; i += 4) {
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+        float4 a = make_float4(other, other, other, other), b = zero;
         if (valid) {
           a = __ldg(reinterpret_cast<const float4*>(row + j + i));
           b = __ldg(reinterpret_cast<const float4*>(row + half + j + i));
         }
         c[i] = a.x; c[i + 1] = a.y; c[i + 2] = a.z; c[i + 3] = a.w;
-        s[i] = low ? -b.x : b.x;
-        s[i + 1] = low ? -b.y : b.y;
-        s[i + 2] = low ? -b.z : b.z;
-        s[i + 3] = low ? -b.w : b.w;
+        const bool neg = low != kBack;
+        s[i] = neg ? -b.x : b.x;
+        s[i + 1] = neg ? -b.y : b.y;
+        s[i + 2] = neg ? -b.z : b.z;
+        s[i + 3] = neg ? -b.w : b.w;
       }
     }
   }
 
-  // z rotated (sign 1) or rotated back (sign -1), in place; every lane of the warp calls it.
-  __device__ __forceinline__ void apply(float (&z)[8], float sign) const {
-    float zp[8];
+  // The partners of this lane's packed values, as floats, 0 where nothing rotates (what lies
+  // there may be infinite, and a coefficient of 0 would make it NaN); every lane of the warp
+  // calls it.  The mask costs nothing: it is part of the unpacking.
+  __device__ __forceinline__ void partners(const uint4& x, float (&y)[8]) const {
+    const uint32_t low = rotates ? 0x10000u : 0u, high = rotates ? 0xffff0000u : 0u;
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      zp[i] = kInter ? z[i ^ 1] : __shfl_sync(0xffffffffu, z[i], partner);
-    if (!rotates) return;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = fmaf(z[i], c[i], zp[i] * (sign * s[i]));
+    for (int i = 0; i < 4; ++i) {
+      if (kInter) {
+        y[2 * i] = __uint_as_float(w[i] & high);
+        y[2 * i + 1] = __uint_as_float(w[i] * low);
+      } else {
+        w[i] = __shfl_sync(0xffffffffu, w[i], partner);
+        y[2 * i] = __uint_as_float(w[i] * low);
+        y[2 * i + 1] = __uint_as_float(w[i] & high);
+      }
+    }
+  }
+};
+
+// 1 / sqrt of a mean square plus eps (a normal number: the host refuses a smaller eps).
+__device__ __forceinline__ float inv_sqrt(float v) {
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// Chunks of a token: `steps` times the rows of a warp of one kind of head each.
+struct Chunks {
+  int rows, q, kv;      // rows of a chunk; chunks of the query, and of the key or value heads
+
+  __host__ __device__ Chunks(int Hq, int Hkv, int warp_rows, int steps)
+      : rows(warp_rows * steps), q((Hq + rows - 1) / rows), kv((Hkv + rows - 1) / rows) {}
+  __host__ __device__ int all() const { return q + 2 * kv; }
+};
+
+enum { kQuery = 0, kKey = 1, kValue = 2 };
+
+// Chunk c as its kind and its rows [h0, h1) among the heads of that kind.
+struct Span {
+  int kind, h0, h1, heads;
+
+  __device__ __forceinline__ Span(const Chunks& ch, int c, int Hq, int Hkv) {
+    kind = c < ch.q ? kQuery : c < ch.q + ch.kv ? kKey : kValue;
+    heads = kind == kQuery ? Hq : Hkv;
+    h0 = (kind == kQuery ? c : kind == kKey ? c - ch.q : c - ch.q - ch.kv) * ch.rows;
+    h1 = min(h0 + ch.rows, heads);
   }
 };
 
 template <int D, bool kNorm, bool kInter, bool kPaged>
-__global__ void __launch_bounds__(kPrepThreads, 3) attn_qk_prep_kernel(const PrepParams p) {
+__global__ void __launch_bounds__(kPrepThreads, kFwdBlocks)
+attn_qk_prep_kernel(const PrepParams p, int steps) {
   using R = Row<D>;
+  __shared__ __align__(16) uint4 rows[kChunkSteps][kPrepThreads];
   const int lane = threadIdx.x & 31;
   const int sub = lane / R::kLanes, e0 = (lane % R::kLanes) * 8;
-  constexpr int kItemRows = kFwdSteps * R::kRows;
-  const int bpt = (p.H + kItemRows - 1) / kItemRows;     // items a token
+  const Chunks ch(p.Hq, p.Hkv, R::kRows, steps);
   const unsigned item = blockIdx.x * kPrepWarps + (threadIdx.x >> 5);
-  const int t = (int)(item / (unsigned)bpt);
+  const int t = (int)(item / (unsigned)ch.all());
   if (t >= p.tokens) return;
-  const int h0 = (int)(item % (unsigned)bpt) * kItemRows + sub;
+  const Span sp(ch, (int)(item - (unsigned)t * ch.all()), p.Hq, p.Hkv);
+  const int kind = sp.kind;
+  const uint32_t mine = smem_u32(&rows[0][threadIdx.x]);
+  constexpr uint32_t kSlot = kPrepThreads * 16;
 
-  uint4 x[kFwdSteps];
-  const size_t in0 = ((size_t)t * p.H + h0) * D + e0;
+  {
+    const int head0 = kind == kQuery ? 0 : kind == kKey ? p.Hq : p.Hq + p.Hkv;
+    const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.qkv) +
+                               ((size_t)t * p.H + head0) * D + e0;
 #pragma unroll
-  for (int i = 0; i < kFwdSteps; ++i) {
-    x[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (h0 + i * R::kRows < p.H) x[i] = load_once(p.qkv, in0 + (size_t)i * R::kRows * D);
+    for (int i = 0; i < kChunkSteps; ++i) {
+      const int h = sp.h0 + i * R::kRows + sub;
+      if (i < steps) copy16(mine + i * kSlot, src + min(h, sp.h1 - 1) * D, h < sp.h1);
+      if (i == kChunkSteps / 2 - 1 || i == kChunkSteps - 1) copy_commit();
+    }
   }
-  const int n = kPaged ? 0 : t % p.N, b = kPaged ? 0 : t / p.N;
-  Angles<kInter> ang;
-  ang.load(p, p.positions != nullptr ? __ldg(p.positions + t) : n, e0, lane);
-  uint4 wq = make_uint4(0u, 0u, 0u, 0u), wk = wq;
-  if (kNorm) {
-    wq = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.wq) + e0));
-    wk = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.wk) + e0));
-  }
-  int slot = -1;
-  size_t kv0 = 0;            // first element of this token's row in KV head 0's pages
+
+  // this lane's part of the token's row of head h0 + sub, and what the next step adds
+  size_t dst, dst_step;
+  bool keep = true;
+  int pos;
   if (kPaged) {
-    const long long s = __ldg(p.slots + t);
-    if (s >= 0 && s < p.num_slots) {
-      slot = (int)s;
-      const int page = slot / p.page_size;
-      kv0 = ((size_t)page * p.Hkv * p.page_size + (size_t)(slot - page * p.page_size)) * D;
+    pos = __ldg(p.positions + t);
+    if (kind == kQuery) {
+      dst = (size_t)t * p.Hq * D;
+      dst_step = D;
+    } else {
+      const long long s = __ldg(p.slots + t);
+      keep = s >= 0 && s < p.num_slots;
+      const int place = keep ? (int)s : 0;
+      const int page = place / p.page_size;
+      dst = ((size_t)page * p.Hkv * p.page_size + (size_t)(place - page * p.page_size)) * D;
+      dst_step = (size_t)p.page_size * D;
+    }
+  } else {
+    const int b = t / p.N, n = t - b * p.N;
+    pos = p.positions != nullptr ? __ldg(p.positions + t) : n;
+    dst = ((size_t)b * sp.heads * p.N + n) * D;
+    dst_step = (size_t)p.N * D;
+  }
+  __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(kind == kQuery ? p.q
+                                                        : kind == kKey ? p.k : p.v) +
+                       dst + (sp.h0 + sub) * dst_step + e0;
+  dst_step *= R::kRows;
+  // rows of this lane in the chunk (0: the token has no place)
+  const int n_rows = keep && sp.h0 + sub < sp.h1 ? (sp.h1 - sp.h0 - sub - 1) / R::kRows + 1 : 0;
+  const int n_steps = (sp.h1 - sp.h0 - 1) / R::kRows + 1;
+
+  Angles<kInter> ang;
+  if (kind != kValue) {
+    ang.place(p, e0, lane);
+    ang.template load<false>(p, pos, e0);
+    if (kNorm) {      // A = w c, B = w_partner s
+      const uint4 w = load_gain(kind == kQuery ? p.wq : p.wk, e0);
+      float g[8];
+      unpack8(w, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ang.c[j] *= g[j];
+      ang.partners(w, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ang.s[j] *= g[j];
     }
   }
-
 #pragma unroll
-  for (int i = 0; i < kFwdSteps; ++i) {
-    const int h = h0 + i * R::kRows;
-    const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
-    uint4 out = x[i];
-    if (h - sub < p.Hq + p.Hkv) {      // the warp's rows are not all V (warp-uniform)
-      float z[8];
-      unpack8(x[i], z);
-      if (kNorm) {
-        float ss = 0.f;
+  for (int half = 0; half < 2; ++half) {
+    half == 0 ? copy_wait<1>() : copy_wait<0>();
+    const int end = half == 0 ? min(n_steps, kChunkSteps / 2) : n_steps;
+#pragma unroll 1
+    for (int i = half * (kChunkSteps / 2); i < end; ++i) {
+      uint4 x = read16(mine + i * kSlot);
+      if (kind != kValue) {
+        float v[8], vp[8];
+        unpack8(x, v);
+        ang.partners(x, vp);
+        float r = 1.f;
+        if (kNorm) {
+          float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(z[j], z[j], ss);
-        const float r = rsqrtf(row_sum<R::kLanes>(ss) * (1.0f / D) + p.eps);
-        float w[8];
-        unpack8(is_q ? wq : wk, w);
+          for (int j = 0; j < 8; j += 2) ffma2(s0, s1, v[j], v[j + 1], v[j], v[j + 1], s0, s1);
+          r = inv_sqrt(row_sum<R::kLanes>(s0 + s1) * (1.0f / D) + p.eps);
+        }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) z[j] *= r * w[j];
+        for (int j = 0; j < 8; j += 2) {
+          fmul2(v[j], v[j + 1], v[j], v[j + 1], ang.c[j], ang.c[j + 1]);
+          ffma2(v[j], v[j + 1], vp[j], vp[j + 1], ang.s[j], ang.s[j + 1], v[j], v[j + 1]);
+          if (kNorm) fmul2(v[j], v[j + 1], v[j], v[j + 1], r, r);
+        }
+        x = pack8(v);
       }
-      ang.apply(z, 1.f);
-      if (!is_v) out = pack8(z);
-    }
-    if (h >= p.H) continue;
-    if (kPaged) {
-      if (is_q) {
-        store8(p.q, ((size_t)t * p.Hq + h) * D + e0, out);
-      } else if (slot >= 0) {
-        const int hk = is_v ? h - p.Hq - p.Hkv : h - p.Hq;
-        store8(is_v ? p.v : p.k, kv0 + (size_t)hk * p.page_size * D + e0, out);
-      }
-    } else {
-      if (is_q) {
-        store8(p.q, (((size_t)b * p.Hq + h) * p.N + n) * D + e0, out);
-      } else {
-        const int hk = is_v ? h - p.Hq - p.Hkv : h - p.Hq;
-        store8(is_v ? p.v : p.k, (((size_t)b * p.Hkv + hk) * p.N + n) * D + e0, out);
-      }
+      if (i < n_rows) store8(out, 0, x);
+      out += dst_step;
     }
   }
 }
 
-// Backward.  The grid is persistent so that a warp keeps its share of the gains' gradients in
-// registers over all its rows; a block adds its warps' shares in shared memory and leaves one
-// partial, and a second kernel adds the partials in a fixed order (no atomics: the same
-// inputs give the same bits).
+// Backward.  A block takes a run of tokens and goes through their query chunks, then their key
+// chunks, then their value chunks, each kind spread evenly over its warps.  A warp so keeps
+// its share of one gain's gradient in registers over all its rows of that kind; the block
+// adds its warps' shares in shared memory and leaves one partial, and a second kernel adds the
+// partials in a fixed order (no atomics: the same inputs give the same bits).  While a step
+// is computed, the same step of the warp's next chunk is on its way.
 template <int D, bool kNorm, bool kInter>
-__global__ void __launch_bounds__(kPrepThreads) attn_qk_prep_bwd_kernel(const PrepBwdParams pb) {
+__global__ void __launch_bounds__(kPrepThreads, kBwdBlocks)
+attn_qk_prep_bwd_kernel(const PrepBwdParams pb, int steps) {
   using R = Row<D>;
   const PrepParams& p = pb.f;
+  extern __shared__ __align__(16) uint4 bwd_rows[];      // [steps][x, dy][kPrepThreads]
   __shared__ float acc_s[kNorm ? kPrepWarps : 1][2][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / R::kLanes, e0 = (lane % R::kLanes) * 8;
-  constexpr int kItemRows = kBwdSteps * R::kRows;
-  const int bpt = (p.H + kItemRows - 1) / kItemRows;
-  const unsigned items = (unsigned)p.tokens * (unsigned)bpt;
-  uint4 wq = make_uint4(0u, 0u, 0u, 0u), wk = wq;
-  if (kNorm) {
-    wq = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.wq) + e0));
-    wk = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.wk) + e0));
-  }
-  float aq[8], ak[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) aq[j] = ak[j] = 0.f;
+  const uint32_t mine = smem_u32(bwd_rows + threadIdx.x);
+  constexpr uint32_t kHalf = kPrepThreads * 16, kSlot = 2 * kHalf;
+  const int t_begin = (int)((long long)blockIdx.x * p.tokens / gridDim.x);
+  const int t_end = (int)(((long long)blockIdx.x + 1) * p.tokens / gridDim.x);
 
-  for (unsigned item = blockIdx.x * kPrepWarps + warp; item < items;
-       item += gridDim.x * kPrepWarps) {
-    const int t = (int)(item / (unsigned)bpt);
-    const int h0 = (int)(item % (unsigned)bpt) * kItemRows + sub;
-    const int n = t % p.N, b = t / p.N;
-    uint4 x[kBwdSteps], dy[kBwdSteps];
-    const size_t in0 = ((size_t)t * p.H + h0) * D + e0;
+  Angles<kInter> ang;
+  ang.place(p, e0, lane);
+
+#pragma unroll 1
+  for (int kind = kQuery; kind <= kValue; ++kind) {
+    const int heads = kind == kQuery ? p.Hq : p.Hkv;
+    const int head0 = kind == kQuery ? 0 : kind == kKey ? p.Hq : p.Hq + p.Hkv;
+    const int n_steps = min(steps, (heads + R::kRows - 1) / R::kRows);
+    const int chunk = n_steps * R::kRows;
+    const int chunks = heads > 0 ? (heads + chunk - 1) / chunk : 0;
+    const int items = (t_end - t_begin) * chunks;
+    const bool x_too = kNorm && kind != kValue;
+    const __nv_bfloat16* dy_of = reinterpret_cast<const __nv_bfloat16*>(kind == kQuery ? p.q
+                                                                        : kind == kKey ? p.k : p.v);
+    float w[8], acc[8];
 #pragma unroll
-    for (int i = 0; i < kBwdSteps; ++i) {
-      const int h = h0 + i * R::kRows;
-      x[i] = dy[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (h < p.H) {
-        if (kNorm && h < p.Hq + p.Hkv) x[i] = load_once(p.qkv, in0 + (size_t)i * R::kRows * D);
-        if (h < p.Hq)
-          dy[i] = load_once(p.q, (((size_t)b * p.Hq + h) * p.N + n) * D + e0);
-        else if (h < p.Hq + p.Hkv)
-          dy[i] = load_once(p.k, (((size_t)b * p.Hkv + h - p.Hq) * p.N + n) * D + e0);
-        else
-          dy[i] = load_once(p.v, (((size_t)b * p.Hkv + h - p.Hq - p.Hkv) * p.N + n) * D + e0);
+    for (int j = 0; j < 8; ++j) w[j] = acc[j] = 0.f;
+    if (x_too) unpack8(load_gain(kind == kQuery ? p.wq : p.wk, e0), w);
+
+    // An item's token, and this lane's first row of it: offsets in the input and the gradient,
+    // and how many of its steps have a row for this lane.
+    int t, n_rows;
+    size_t in, dy_in;
+    auto aim = [&](int item) {
+      t = item / chunks;
+      const int h = (item - t * chunks) * chunk + sub;
+      t += t_begin;
+      const int b = t / p.N;
+      in = ((size_t)t * p.H + head0 + h) * D + e0;
+      dy_in = (((size_t)b * heads + h) * p.N + (t - b * p.N)) * D + e0;
+      n_rows = h < heads ? min((heads - h - 1) / R::kRows + 1, n_steps) : 0;
+    };
+    const __nv_bfloat16 *cx = nullptr, *cdy = nullptr;
+    const __nv_bfloat16* any = reinterpret_cast<const __nv_bfloat16*>(p.qkv);   // for no row
+    const size_t dy_step = (size_t)p.N * D * R::kRows;
+    auto copy_step = [&](int i) {
+      const bool valid = i < n_rows;
+      copy16(mine + i * kSlot + kHalf, valid ? cdy : any, valid);
+      if (x_too) copy16(mine + i * kSlot, valid ? cx : any, valid);
+      cdy += dy_step;
+      cx += R::kRows * D;
+    };
+    auto start = [&](int item) {
+      aim(item);
+      cx = any + in;
+      cdy = dy_of + dy_in;
+    };
+    int item = warp;
+    if (item < items) {
+      start(item);
+      for (int i = 0; i < n_steps; ++i) {
+        copy_step(i);
+        copy_commit();
       }
     }
-    Angles<kInter> ang;
-    ang.load(p, p.positions != nullptr ? __ldg(p.positions + t) : n, e0, lane);
+    for (; item < items; item += kPrepWarps) {
+      if (kind != kValue)
+        ang.template load<true>(p, p.positions != nullptr ? __ldg(p.positions + t) : t % p.N, e0);
+      __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(pb.dqkv) + in;
+      const int rows = n_rows;
+      const bool more = item + kPrepWarps < items;
+      if (more) start(item + kPrepWarps);
+      for (int i = 0; i < n_steps; ++i) {
+        // Copies in flight: this item's steps i .. n - 1 and, of the next, 0 .. i - 2 (a place
+        // is filled again one step after it was read).
+        if (n_steps >= 8) copy_wait<7>();
+        else if (n_steps >= 4) copy_wait<3>();
+        else if (n_steps >= 2) copy_wait<1>();
+        else copy_wait<0>();
+        const uint4 x = x_too ? read16(mine + i * kSlot) : make_uint4(0u, 0u, 0u, 0u);
+        uint4 dy = read16(mine + i * kSlot + kHalf);
+        if (more && i > 0) copy_step(i - 1);
+        copy_commit();
+        if (kind != kValue) {
+          float dz[8], dp[8];
+          unpack8(dy, dz);
+          ang.partners(dy, dp);
 #pragma unroll
-    for (int i = 0; i < kBwdSteps; ++i) {
-      const int h = h0 + i * R::kRows;
-      uint4 out = dy[i];
-      if (h - sub < p.Hq + p.Hkv) {
-        const bool is_q = h < p.Hq, is_v = h >= p.Hq + p.Hkv;
-        float dz[8];
-        unpack8(dy[i], dz);
-        ang.apply(dz, -1.f);
-        if (kNorm) {
-          float xv[8], w[8];
-          unpack8(x[i], xv);
-          unpack8(is_q ? wq : wk, w);
-          float ss = 0.f, st = 0.f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            w[j] *= dz[j];
-            ss = fmaf(xv[j], xv[j], ss);
-            st = fmaf(xv[j], w[j], st);
+          for (int j = 0; j < 8; j += 2) {
+            fmul2(dz[j], dz[j + 1], dz[j], dz[j + 1], ang.c[j], ang.c[j + 1]);
+            ffma2(dz[j], dz[j + 1], dp[j], dp[j + 1], ang.s[j], ang.s[j + 1], dz[j], dz[j + 1]);
           }
-          const float r = rsqrtf(row_sum<R::kLanes>(ss) * (1.0f / D) + p.eps);
-          const float m = row_sum<R::kLanes>(st) * (1.0f / D) * r * r;
+          if (kNorm) {
+            float xv[8], wd[8];
+            unpack8(x, xv);
+            float s0 = 0.f, s1 = 0.f, t0 = 0.f, t1 = 0.f;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float g = dz[j] * xv[j] * r;
-            if (is_q) aq[j] += g;
-            else if (!is_v) ak[j] += g;
-            dz[j] = r * (w[j] - xv[j] * m);
+            for (int j = 0; j < 8; j += 2) {
+              fmul2(wd[j], wd[j + 1], w[j], w[j + 1], dz[j], dz[j + 1]);
+              ffma2(s0, s1, xv[j], xv[j + 1], xv[j], xv[j + 1], s0, s1);
+              ffma2(t0, t1, xv[j], xv[j + 1], wd[j], wd[j + 1], t0, t1);
+            }
+            const float r = inv_sqrt(row_sum<R::kLanes>(s0 + s1) * (1.0f / D) + p.eps);
+            const float m = row_sum<R::kLanes>(t0 + t1) * (-1.0f / D) * r * r;
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+              ffma2(wd[j], wd[j + 1], xv[j], xv[j + 1], m, m, wd[j], wd[j + 1]);
+              fmul2(xv[j], xv[j + 1], xv[j], xv[j + 1], r, r);
+              ffma2(acc[j], acc[j + 1], dz[j], dz[j + 1], xv[j], xv[j + 1], acc[j], acc[j + 1]);
+              fmul2(dz[j], dz[j + 1], wd[j], wd[j + 1], r, r);
+            }
           }
+          dy = pack8(dz);
         }
-        if (!is_v) out = pack8(dz);
+        if (i < rows) store8(to, 0, dy);
+        to += R::kRows * D;
       }
-      if (h < p.H) store8(pb.dqkv, in0 + (size_t)i * R::kRows * D, out);
+      if (more) copy_step(n_steps - 1);
+      copy_commit();
+    }
+    copy_wait<0>();
+
+    if (x_too) {
+#pragma unroll
+      for (int o = R::kLanes; o < 32; o <<= 1)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
+      if (sub == 0) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc_s[warp][kind][e0 + j] = acc[j];
+      }
     }
   }
-
   if (kNorm) {
-#pragma unroll
-    for (int o = R::kLanes; o < 32; o <<= 1)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        aq[j] += __shfl_xor_sync(0xffffffffu, aq[j], o);
-        ak[j] += __shfl_xor_sync(0xffffffffu, ak[j], o);
-      }
-    if (sub == 0) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        acc_s[warp][0][e0 + j] = aq[j];
-        acc_s[warp][1][e0 + j] = ak[j];
-      }
-    }
     __syncthreads();
     for (int c = threadIdx.x; c < 2 * D; c += kPrepThreads) {
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < kPrepWarps; ++w) s += acc_s[w][c / D][c % D];
+      for (int v = 0; v < kPrepWarps; ++v) s += acc_s[v][c / D][c % D];
       pb.partials[(size_t)blockIdx.x * 2 * D + c] = s;
     }
   }
@@ -340,26 +492,39 @@ __global__ void __launch_bounds__(1024) attn_qk_prep_dw_kernel(const float* part
   }
 }
 
+// Steps of a chunk: many for a large call, so that the angles are read and multiplied seldom,
+// fewer while that leaves SMs without warps.
+int chunk_steps(long long tokens, int Hq, int Hkv, int warp_rows, int num_sms) {
+  int steps = kChunkSteps;
+  while (steps > 1 &&
+         tokens * Chunks(Hq, Hkv, warp_rows, steps).all() < (long long)num_sms * 16)
+    steps /= 2;
+  return steps;
+}
+
 template <int D, bool kNorm, bool kInter>
-int launch_fwd_t(const PrepParams& p, bool paged, cudaStream_t stream) {
-  constexpr int kItemRows = kFwdSteps * Row<D>::kRows;
-  const long long items = (long long)p.tokens * ((p.H + kItemRows - 1) / kItemRows);
-  const long long blocks = (items + kPrepWarps - 1) / kPrepWarps;   // items < 2^31 (host check)
+int launch_fwd_t(const PrepParams& p, bool paged, int num_sms, cudaStream_t stream) {
+  const int steps = chunk_steps(p.tokens, p.Hq, p.Hkv, Row<D>::kRows, num_sms);
+  const long long items = (long long)p.tokens * Chunks(p.Hq, p.Hkv, Row<D>::kRows, steps).all();
+  const unsigned blocks = (unsigned)((items + kPrepWarps - 1) / kPrepWarps);   // items < 2^31
   if (paged)
-    attn_qk_prep_kernel<D, kNorm, kInter, true><<<(unsigned)blocks, kPrepThreads, 0, stream>>>(p);
+    attn_qk_prep_kernel<D, kNorm, kInter, true><<<blocks, kPrepThreads, 0, stream>>>(p, steps);
   else
-    attn_qk_prep_kernel<D, kNorm, kInter, false><<<(unsigned)blocks, kPrepThreads, 0, stream>>>(p);
+    attn_qk_prep_kernel<D, kNorm, kInter, false><<<blocks, kPrepThreads, 0, stream>>>(p, steps);
   return cudaGetLastError() == cudaSuccess ? 0 : -4;
 }
 
 template <int D, bool kNorm, bool kInter>
 int launch_bwd_t(const PrepBwdParams& p, int num_sms, cudaStream_t stream) {
-  constexpr int kItemRows = kBwdSteps * Row<D>::kRows;
-  const long long items = (long long)p.f.tokens * ((p.f.H + kItemRows - 1) / kItemRows);
-  long long blocks = (items + kPrepWarps - 1) / kPrepWarps;
-  if (blocks > 4LL * num_sms) blocks = 4LL * num_sms;
-  if (blocks > kPrepBwdMaxBlocks) blocks = kPrepBwdMaxBlocks;
-  attn_qk_prep_bwd_kernel<D, kNorm, kInter><<<(unsigned)blocks, kPrepThreads, 0, stream>>>(p);
+  const int steps = chunk_steps(p.f.tokens, p.f.Hq, p.f.Hkv, Row<D>::kRows, num_sms);
+  const long long blocks = std::min<long long>(
+      p.f.tokens, std::min<long long>((long long)kBwdBlocks * num_sms, kPrepBwdMaxBlocks));
+  const int smem = steps * 2 * kPrepThreads * 16;
+  auto kernel = attn_qk_prep_bwd_kernel<D, kNorm, kInter>;
+  static std::atomic<bool> ready[64];
+  if (!allow_smem(reinterpret_cast<const void*>(kernel), kChunkSteps * 2 * kPrepThreads * 16, ready))
+    return -4;
+  kernel<<<(unsigned)blocks, kPrepThreads, smem, stream>>>(p, steps);
   if (cudaGetLastError() != cudaSuccess) return -4;
   if (kNorm) {
     attn_qk_prep_dw_kernel<<<2 * D / 32, 1024, 0, stream>>>(p.partials, (int)blocks, D, p.dwq,
@@ -370,12 +535,12 @@ int launch_bwd_t(const PrepBwdParams& p, int num_sms, cudaStream_t stream) {
 }
 
 template <int D>
-int launch_fwd_d(const PrepParams& p, bool paged, cudaStream_t s) {
+int launch_fwd_d(const PrepParams& p, bool paged, int num_sms, cudaStream_t s) {
   if (p.wq != nullptr)
-    return p.interleaved ? launch_fwd_t<D, true, true>(p, paged, s)
-                         : launch_fwd_t<D, true, false>(p, paged, s);
-  return p.interleaved ? launch_fwd_t<D, false, true>(p, paged, s)
-                       : launch_fwd_t<D, false, false>(p, paged, s);
+    return p.interleaved ? launch_fwd_t<D, true, true>(p, paged, num_sms, s)
+                         : launch_fwd_t<D, true, false>(p, paged, num_sms, s);
+  return p.interleaved ? launch_fwd_t<D, false, true>(p, paged, num_sms, s)
+                       : launch_fwd_t<D, false, false>(p, paged, num_sms, s);
 }
 
 template <int D>
@@ -389,9 +554,10 @@ int launch_bwd_d(const PrepBwdParams& p, int num_sms, cudaStream_t s) {
 
 }  // namespace
 
-int launch_qk_prep(const PrepParams& p, int d, bool paged, cudaStream_t stream) {
+int launch_qk_prep(const PrepParams& p, int d, bool paged, int num_sms, cudaStream_t stream) {
   if (p.tokens <= 0) return 0;
-  return d == 128 ? launch_fwd_d<128>(p, paged, stream) : launch_fwd_d<64>(p, paged, stream);
+  return d == 128 ? launch_fwd_d<128>(p, paged, num_sms, stream)
+                  : launch_fwd_d<64>(p, paged, num_sms, stream);
 }
 
 int launch_qk_prep_bwd(const PrepBwdParams& p, int d, int num_sms, cudaStream_t stream) {

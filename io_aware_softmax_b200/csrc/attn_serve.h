@@ -2,6 +2,7 @@
 // preparation, tree attention) shared by their launch wrappers and the C-ABI entry points.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -9,8 +10,22 @@
 
 namespace attn {
 
-// Sequences of one attn_page_tables call: two prefix sums of 4 bytes each stay in shared
-// memory (128 KB at this bound).
+// Allows a kernel `bytes` of dynamic shared memory, once a device (ready: one flag a device,
+// of this kernel alone): the attribute keeps, and setting it costs host time in every call.
+inline bool allow_smem(const void* kernel, int bytes, std::atomic<bool> (&ready)[64]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const bool known = dev >= 0 && dev < 64;
+  if (known && ready[dev].load(std::memory_order_acquire)) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+      cudaSuccess)
+    return false;
+  if (known) ready[dev].store(true, std::memory_order_release);
+  return true;
+}
+
+// Sequences of one attn_page_tables call: 12 bytes each stay in shared memory (192 KB at this
+// bound).
 constexpr int kPagesMaxSeqs = 16384;
 
 struct PagesParams {
@@ -26,6 +41,8 @@ struct PagesParams {
   int* token_offsets;       // [B + 1] (written)
   int* pages_used;          // [1] (written)
   int B, max_pages, page_size, num_free, num_tokens;
+  unsigned div_mul;         // row / page_size = row * div_mul >> div_shift (set by the launch)
+  int div_shift;
 };
 
 struct PrepParams {
@@ -53,7 +70,9 @@ struct PrepBwdParams {
   float* dwk;
 };
 
-// Blocks of the backward at most: the workspace holds one partial gain gradient for each.
+// Heads of a token at most (query, key and value), and blocks of the backward: the workspace
+// holds one partial gain gradient for each block.
+constexpr int kPrepMaxHeads = 4096;
 constexpr int kPrepBwdMaxBlocks = 592;
 
 // Nodes of a sequence at most (a node's visible nodes are a 128-bit word), and rows of one
@@ -82,7 +101,7 @@ struct TreeParams {
 };
 
 int launch_page_tables(const PagesParams& p, int num_sms, cudaStream_t stream);
-int launch_qk_prep(const PrepParams& p, int d, bool paged, cudaStream_t stream);
+int launch_qk_prep(const PrepParams& p, int d, bool paged, int num_sms, cudaStream_t stream);
 int launch_qk_prep_bwd(const PrepBwdParams& p, int d, int num_sms, cudaStream_t stream);
 
 // tq: q as (d, G, Hkv, T) in boxes of 64 x G x 1 x tile_nodes; tk, tv: pages as

@@ -825,8 +825,8 @@ int launch_tree_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMa
                   const TreeParams& p, cudaStream_t stream) {
   using C = TreeCfg<D, kTwo>;
   static_assert(C::kSmem <= 227 * 1024, "shared memory budget");
-  if (cudaFuncSetAttribute(attn_tree_kernel<D, kTwo>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           C::kSmem) != cudaSuccess)
+  static std::atomic<bool> ready[64];
+  if (!allow_smem(reinterpret_cast<const void*>(&attn_tree_kernel<D, kTwo>), C::kSmem, ready))
     return -4;
   attn_tree_kernel<D, kTwo><<<p.grid, kTreeThreads, C::kSmem, stream>>>(tq, tk, tv, p);
   if (cudaGetLastError() != cudaSuccess) return -4;
