@@ -442,6 +442,13 @@ def _given(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, ref:
         _out(t, name, dtype, shape, ref)
 
 
+def _dims(t: torch.Tensor, name: str, dtype: torch.dtype, dims: int):
+    """t's shape, which must have ``dims`` entries (the rest is _given's to check)."""
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        _need(t, name, dtype, dims)
+    return t.shape
+
+
 def _optional(t, name: str, dtype: torch.dtype, shape, ref: torch.Tensor):
     if t is not None:
         _given(t, name, dtype, shape, ref)
@@ -474,28 +481,35 @@ def attn_page_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages:
     lib = _lib.load()
     i32 = torch.int32
     _need(ctx_lens, "ctx_lens", i32, 1)
-    _need(free_pages, "free_pages", i32, 1)
-    _need(block_table, "block_table", i32, 2)
-    B, max_pages, T = ctx_lens.shape[0], block_table.shape[1], int(num_tokens)
+    B, T = ctx_lens.shape[0], int(num_tokens)
     if T < 0:
         raise ValueError("num_tokens must not be negative")
-    if block_table.shape[0] != B:
-        raise ValueError("block_table needs one row per sequence")
-    _same_device(ctx_lens, (free_pages, "free_pages"), (block_table, "block_table"))
+    num_free, = _dims(free_pages, "free_pages", i32, 1)
+    _, max_pages = _dims(block_table, "block_table", i32, 2)
+    _given(free_pages, "free_pages", i32, (num_free,), ctx_lens)
+    _given(block_table, "block_table", i32, (B, max_pages), ctx_lens)
     _given(new_lens, "new_lens", i32, (B,), ctx_lens)
     _optional(free_used, "free_used", i32, (1,), ctx_lens)
     _optional(parents, "parents", i32, (T,), ctx_lens)
     slots = _result(slots, "slots", torch.int64, (T,), ctx_lens)
-    positions = _result(positions, "positions", i32, (T,), ctx_lens)
-    seq_lens = _result(seq_lens, "seq_lens", i32, (B,), ctx_lens)
-    token_offsets = _result(token_offsets, "token_offsets", i32, (B + 1,), ctx_lens)
-    pages_used = _result(pages_used, "pages_used", i32, (1,), ctx_lens)
+    if positions is seq_lens is token_offsets is pages_used is None:
+        # one allocation for the four int32 results: a view costs less host time
+        buf = ctx_lens.new_empty(T + 2 * B + 2)
+        positions = buf.as_strided((T,), (1,), 0)
+        seq_lens = buf.as_strided((B,), (1,), T)
+        token_offsets = buf.as_strided((B + 1,), (1,), T + B)
+        pages_used = buf.as_strided((1,), (1,), T + 2 * B + 1)
+    else:
+        positions = _result(positions, "positions", i32, (T,), ctx_lens)
+        seq_lens = _result(seq_lens, "seq_lens", i32, (B,), ctx_lens)
+        token_offsets = _result(token_offsets, "token_offsets", i32, (B + 1,), ctx_lens)
+        pages_used = _result(pages_used, "pages_used", i32, (1,), ctx_lens)
     with _device(ctx_lens):
         st = lib.attn_page_tables(_ptr(ctx_lens), _ptr(new_lens), _ptr(free_pages),
                                   _ptr(free_used), _ptr(parents), _ptr(block_table), _ptr(slots),
                                   _ptr(positions), _ptr(seq_lens), _ptr(token_offsets),
                                   _ptr(pages_used), B, max_pages, int(page_size),
-                                  free_pages.shape[0], T, _stream(ctx_lens.device, stream))
+                                  num_free, T, _stream(ctx_lens.device, stream))
     _check(st, "attn_page_tables")
     return slots, positions, seq_lens, token_offsets, pages_used
 
@@ -563,9 +577,7 @@ def attn_qk_norm_rope_bwd(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
     rot, rows = _prep_inputs(qkv, 4, q_weight, k_weight, rope_table)
     B, N, H, d = qkv.shape
     bf16 = torch.bfloat16
-    _need(dq, "dq", bf16, 4)
-    _need(dk, "dk", bf16, 4)
-    Hq, Hkv = dq.shape[1], dk.shape[1]
+    Hq, Hkv = _dims(dq, "dq", bf16, 4)[1], _dims(dk, "dk", bf16, 4)[1]
     if Hq + 2 * Hkv != H:
         raise ValueError(f"dq and dk have {Hq} and {Hkv} heads, qkv {H}")
     _given(dq, "dq", bf16, (B, Hq, N, d), qkv)
@@ -614,10 +626,10 @@ def attn_qk_norm_rope_paged(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
     rot, rows = _prep_inputs(qkv, 3, q_weight, k_weight, rope_table)
     T, H, d = qkv.shape
     bf16 = torch.bfloat16
-    _need(k_pages, "k_pages", bf16, 4)
-    num_pages, Hkv, page_size, _ = k_pages.shape
-    _given(k_pages, "k_pages", bf16, (num_pages, Hkv, page_size, d), qkv)
-    _given(v_pages, "v_pages", bf16, (num_pages, Hkv, page_size, d), qkv)
+    num_pages, Hkv, page_size, _ = _dims(k_pages, "k_pages", bf16, 4)
+    shape = (num_pages, Hkv, page_size, d)
+    _given(k_pages, "k_pages", bf16, shape, qkv)
+    _given(v_pages, "v_pages", bf16, shape, qkv)
     Hq = H - 2 * Hkv
     if Hq <= 0:
         raise ValueError(f"qkv has {H} heads: none for queries beside {Hkv} key and value heads")
@@ -655,14 +667,13 @@ def attn_decode_tree(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
     lib = _lib.load()
     bf16, i32 = torch.bfloat16, torch.int32
     _need(q, "q", bf16, 3)
-    _need(k_pages, "k_pages", bf16, 4)
-    _need(block_table, "block_table", i32, 2)
     T, Hq, d = q.shape
-    num_pages, Hkv, page_size, _ = k_pages.shape
-    B, max_pages = block_table.shape
-    _given(k_pages, "k_pages", bf16, (num_pages, Hkv, page_size, d), q)
-    _given(v_pages, "v_pages", bf16, (num_pages, Hkv, page_size, d), q)
-    _same_device(q, (block_table, "block_table"))
+    num_pages, Hkv, page_size, _ = _dims(k_pages, "k_pages", bf16, 4)
+    B, max_pages = _dims(block_table, "block_table", i32, 2)
+    shape = (num_pages, Hkv, page_size, d)
+    _given(k_pages, "k_pages", bf16, shape, q)
+    _given(v_pages, "v_pages", bf16, shape, q)
+    _given(block_table, "block_table", i32, (B, max_pages), q)
     _given(seq_lens, "seq_lens", i32, (B,), q)
     _given(token_offsets, "token_offsets", i32, (B + 1,), q)
     _optional(parents, "parents", i32, (T,), q)

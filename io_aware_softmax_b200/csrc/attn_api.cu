@@ -884,7 +884,7 @@ extern "C" int attn_decode_tree(const void* q, const void* k_pages, const void* 
                            (plan.tile_nodes * plan.tiles);
   if (cap > (1LL << 31) - 1 - 256 || (long long)num_pages * Hkv > (1LL << 31) - 1 ||
       (long long)T * Hq > (1LL << 31) - 1 ||
-      blocks * Hkv * std::max((cap + 127) / 128, 1LL) > (1LL << 31) - 1)
+      Hkv > 65535 || blocks * Hkv * ((cap + 127) / 128 + 8) > (1LL << 31) - 1)
     return ATTN_ERR_UNSUPPORTED;
   if (workspace == nullptr || workspace_bytes < plan.bytes) return ATTN_ERR_WORKSPACE;
   if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;

@@ -89,7 +89,7 @@ struct TreeParams {
   float* lse;               // fp32 [T, Hq]
   // workspace: prefix sums of the sequences' units, then the pieces' partial results
   long long* prefix;        // [B + 1]
-  float* o_part;            // [2 grid, tiles a CTA, 128, d]: sums of exp(x - m) V
+  float* o_part;            // [2 grid, tiles a CTA, d / 4, 128, 4]: sums of exp(x - m) V
   float2* ml_part;          // [2 grid, tiles a CTA, 128]: (m in base 2, l)
   int B, T, Hq, Hkv, G;
   int page_size, max_pages, num_pages, max_nodes;
