@@ -226,6 +226,8 @@ attn_qk_prep_kernel(const PrepParams p, int steps) {
   const int kind = sp.kind;
   const uint32_t mine = smem_u32(&rows[0][threadIdx.x]);
   constexpr uint32_t kSlot = kPrepThreads * 16;
+  // the first of two loads, one after the other, on the way to the angles
+  const int pos = kPaged || p.positions != nullptr ? __ldg(p.positions + t) : t % p.N;
 
   {
     const int head0 = kind == kQuery ? 0 : kind == kKey ? p.Hq : p.Hq + p.Hkv;
@@ -242,9 +244,7 @@ attn_qk_prep_kernel(const PrepParams p, int steps) {
   // this lane's part of the token's row of head h0 + sub, and what the next step adds
   size_t dst, dst_step;
   bool keep = true;
-  int pos;
   if (kPaged) {
-    pos = __ldg(p.positions + t);
     if (kind == kQuery) {
       dst = (size_t)t * p.Hq * D;
       dst_step = D;
@@ -258,7 +258,6 @@ attn_qk_prep_kernel(const PrepParams p, int steps) {
     }
   } else {
     const int b = t / p.N, n = t - b * p.N;
-    pos = p.positions != nullptr ? __ldg(p.positions + t) : n;
     dst = ((size_t)b * sp.heads * p.N + n) * D;
     dst_step = (size_t)p.N * D;
   }
