@@ -21,10 +21,12 @@
 //   * warp 8 issues S = Q K^T and O += P V, P read from tensor memory; before the product of
 //     a sequence's last tile it zeroes the V rows past the end: what a page holds there may
 //     be anything, and 0 * NaN would reach the sum;
-//   * two softmax warpgroups, a thread a row.  With n G <= 128 rows there is one query tile
-//     and the warpgroups take its key tiles in turn (t = tile parity), each with its own
-//     score, max, sum and O; they join the two O's from tensor memory at the end of a piece.
-//     With more rows each warpgroup has a query tile of its own and every K/V tile feeds both.
+//   * two softmax warpgroups, a thread a row.  With n G <= 128 rows there is one query tile;
+//     each warpgroup takes one half of every key tile, with its own max, sum and O, and the
+//     two O's are joined from tensor memory at the end of a piece.  A thread then has 64
+//     scores of a tile and two tiles' scores are in tensor memory at a time, so that the way
+//     from scores to product (half as long) does not hold up the loads.  With more rows each
+//     warpgroup has a query tile of its own and every K/V tile feeds both.
 // Scores keep fp32; P is rounded to bf16 for the product (2^-8 relative, as in the prefill
 // kernel), its row sum is taken before the rounding.
 #include <cuda.h>
@@ -58,6 +60,7 @@ constexpr uint32_t kNegInf = 0xff800000u;
 enum : uint32_t {
   kSiteTreeQ = 201, kSiteTreeEmpty, kSiteTreeFullK, kSiteTreeFullV, kSiteTreeP, kSiteTreeS,
   kSiteTreeO, kSiteTreeDrain, kSiteTreeQFree, kSiteTreeAlign,
+  kSiteTreePv,
 };
 
 template <int D, bool kTwo>
@@ -70,8 +73,8 @@ struct TreeCfg {
   static constexpr int kRing = kQTiles * kTile;
   static constexpr int kMl = kRing + kStages * kTile;      // float2 [2][128]: (m, l)
   static constexpr int kBar = kMl + 2 * 128 * 8;
-  // barriers: q[2], q_free[2], full[S], empty[S], s[2], p[2][2], o[2], done
-  static constexpr int kNumBars = 13 + 2 * kStages;
+  // barriers: q[2], q_free[2], full[S], empty[S], s[2], p[2][2], o[2], done, pv[2]
+  static constexpr int kNumBars = 15 + 2 * kStages;
   static constexpr int kSlot = kBar + kNumBars * 8;        // tmem slot, abort flag, wait limit
   static constexpr int kStart = kSlot + 16;                // CTA's first sequence, prefixes
   static constexpr int kState = kStart + 32 + kTreeWarps * 8;   // Run [8]: softmax warps'
@@ -203,14 +206,27 @@ __device__ __forceinline__ Run plan_run(const TreeParams& p, int block_nodes, lo
   return *out;
 }
 
+// Places in the ring, counted from a piece's first, of its K and V tiles.  They are loaded in
+// the order of their use: step j takes V_(j - lag), then K_j.  A V tile loaded beside its K
+// would hold its place for `lag` steps before its product can be issued, and with six places
+// the loads then run out of room (279 us instead of 252 at 16 sequences of 32768 rows).
+template <int kLag>
+struct KvOrder {
+  static __device__ __forceinline__ int k(int j) { return j < kLag ? j : 2 * j - kLag + 1; }
+  static __device__ __forceinline__ int v(int j, int n) {
+    return j + kLag < n ? 2 * j + kLag : n + j;
+  }
+};
+
 // ------------------------------------------------------------------------------- rows
 
 __device__ __forceinline__ float fl(uint32_t u) { return __uint_as_float(u); }
 
-__device__ __forceinline__ float row_max(const uint32_t (&s)[128]) {
+template <int N>
+__device__ __forceinline__ float row_max(const uint32_t (&s)[N]) {
   float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
 #pragma unroll
-  for (int c = 0; c < 128; c += 8) {
+  for (int c = 0; c < N; c += 8) {
     m0 = max3f(m0, fl(s[c]), fl(s[c + 1]));
     m1 = max3f(m1, fl(s[c + 2]), fl(s[c + 3]));
     m2 = max3f(m2, fl(s[c + 4]), fl(s[c + 5]));
@@ -219,9 +235,10 @@ __device__ __forceinline__ float row_max(const uint32_t (&s)[128]) {
   return max3f(m0, m1, fmaxf(m2, m3));
 }
 
-// 2^(x ks - m) of one 64-key half, packed in bf16 pairs; returns its fp32 sum.
-__device__ __forceinline__ float row_exp_half(const uint32_t (&s)[128], int base, float ks,
-                                              float m, uint32_t (&pk)[32]) {
+// 2^(x ks - m) of 64 keys from s[base] on, packed in bf16 pairs; returns their fp32 sum.
+template <int N>
+__device__ __forceinline__ float row_exp_64(const uint32_t (&s)[N], int base, float ks, float m,
+                                            uint32_t (&pk)[32]) {
   float a0 = 0.f, a1 = 0.f, b0 = 0.f, b1 = 0.f;
 #pragma unroll
   for (int c = 0; c < 64; c += 4) {
@@ -236,6 +253,13 @@ __device__ __forceinline__ float row_exp_half(const uint32_t (&s)[128], int base
     pk[(c >> 1) + 1] = pack_bf16x2(e2, e3);
   }
   return (a0 + a1) + (b0 + b1);
+}
+
+__device__ __forceinline__ void tmem_scores(uint32_t taddr, uint32_t (&s)[64]) {
+  tmem_ld_x64(taddr, s);
+}
+__device__ __forceinline__ void tmem_scores(uint32_t taddr, uint32_t (&s)[128]) {
+  tmem_ld_x128(taddr, s);
 }
 
 // Keys of the tile that starts at row k0 which a node sees, bit c for key k0 + c: all of the
@@ -265,6 +289,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                  const __grid_constant__ CUtensorMap tmV, const TreeParams p) {
   using C = TreeCfg<D, kTwo>;
   constexpr int NS = C::kStages;
+  constexpr int kLag = kTwo ? 1 : 2;      // steps from a tile's QK^T to its PV
+  using Order = KvOrder<kLag>;
   // six 32 KB stages leave no room to round the base up: the declaration aligns it
   extern __shared__ __align__(1024) uint8_t base[];
   const uint32_t base_u32 = smem_u32(base);
@@ -275,7 +301,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   const uint32_t sQ = base_u32, sRing = base_u32 + C::kRing, sBar = base_u32 + C::kBar;
   auto bar = [&](int i) -> uint32_t { return sBar + 8u * (uint32_t)i; };
   const int BAR_Q = 0, BAR_QF = 2, BAR_FULL = 4, BAR_EMPTY = 4 + NS, BAR_S = 4 + 2 * NS,
-            BAR_P = 6 + 2 * NS, BAR_O = 10 + 2 * NS, BAR_DONE = 12 + 2 * NS;
+            BAR_P = 6 + 2 * NS, BAR_O = 10 + 2 * NS, BAR_DONE = 12 + 2 * NS,
+            BAR_PV = 13 + 2 * NS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::kSlot);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -295,6 +322,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       mbar_init(bar(BAR_P + 2 * t), 4);
       mbar_init(bar(BAR_P + 2 * t + 1), 4);
       mbar_init(bar(BAR_O + t), 1);
+      mbar_init(bar(BAR_PV + t), 1);
     }
     for (int s = 0; s < NS; ++s) {
       mbar_init(bar(BAR_FULL + s), 1);
@@ -309,6 +337,16 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
+  // Query rows that no load fills are zeros: their products cost the tensor cores less power,
+  // and a long run of calls is clocked by the power limit (43 -> 41 us at 7 sequences of 2500
+  // to 5000 rows, 16 KV heads, 5 query rows each).
+  for (int i = threadIdx.x; i < C::kQTiles * C::kChunks * (kTreeRows - tile_rows) * 8;
+       i += kTreeThreads) {
+    const int part = i / ((kTreeRows - tile_rows) * 8), at = i - part * (kTreeRows - tile_rows) * 8;
+    *reinterpret_cast<uint4*>(base + part * C::kChunkBytes + tile_rows * 128 + at * 16) =
+        make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
   // launched while the kernel before it ends: nothing of memory is read or written before this
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Run run = plan_run(p, block_nodes, reinterpret_cast<long long*>(base + C::kStart + 32),
@@ -332,40 +370,49 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         bool ok = true;
         for_each_piece(p, run, block_nodes, [&](const Piece& pc) {
           const int* table = p.block_table + (size_t)pc.b * p.max_pages;
-          for (int i = 0; ok && i < pc.tiles; ++i) {
-            // each 64-row half of the tile: its page (a half never crosses one), or a
-            // coordinate past the map, which reads zeros, for rows past the sequence or a
-            // page outside the cache
-            int z[2], row[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const long long k = (long long)(pc.tile0 + i) * kKeys + 64 * h;
-              z[h] = p.num_pages * p.Hkv;
-              row[h] = 0;
-              if (k < pc.s.len) {
-                const int pg = (int)(k / p.page_size);
-                const int page = __ldg(table + pg);
-                if ((unsigned)page < (unsigned)p.num_pages) z[h] = page * p.Hkv + pc.hk;
-                row[h] = (int)(k - (long long)pg * p.page_size);
-              }
+          // One 64-row half of a tile: its page (a half never crosses one), or a coordinate
+          // past the map, which reads zeros, for rows past the sequence or a page outside the
+          // cache
+          struct Half {
+            int z, row;
+          };
+          auto find = [&](int tile, int h) -> Half {
+            const int k = tile * kKeys + 64 * h;
+            Half x{p.num_pages * p.Hkv, 0};
+            if (k < pc.s.len) {
+              const int pg = k / p.page_size;
+              const int page = __ldg(table + pg);
+              if ((unsigned)page < (unsigned)p.num_pages) x.z = page * p.Hkv + pc.hk;
+              x.row = k - pg * p.page_size;
             }
+            return x;
+          };
+          auto load = [&](const CUtensorMap* map, const Half (&x)[2]) {
+            const int s = issued % NS, round = issued / NS;
+            if (ok && round > 0)
+              ok = mbar_wait(bar(BAR_EMPTY + s), (round - 1) & 1, abort_flag, p.err, kSiteTreeEmpty);
+            if (!ok) return;
+            mbar_arrive_expect_tx(bar(BAR_FULL + s), C::kTile);
 #pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-              const int s = issued % NS, round = issued / NS;
-              if (round > 0 && !mbar_wait(bar(BAR_EMPTY + s), (round - 1) & 1, abort_flag, p.err,
-                                          kSiteTreeEmpty)) {
-                ok = false;
-                break;
-              }
-              mbar_arrive_expect_tx(bar(BAR_FULL + s), C::kTile);
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
+              for (int c = 0; c < C::kChunks; ++c)
+                tma_load_3d(sRing + s * C::kTile + c * C::kChunkBytes + h * 64 * 128, map,
+                            bar(BAR_FULL + s), c * 64, x[h].row, x[h].z);
+            ++issued;
+          };
+          // in the order of use (KvOrder): V a step or two behind its K
+          Half at[kLag + 1][2];
+          for (int j = 0; ok && j < pc.tiles + kLag; ++j) {
 #pragma unroll
-                for (int c = 0; c < C::kChunks; ++c)
-                  tma_load_3d(sRing + s * C::kTile + c * C::kChunkBytes + h * 64 * 128,
-                              kv ? &tmV : &tmK, bar(BAR_FULL + s), c * 64, row[h], z[h]);
-              ++issued;
-            }
+            for (int i = kLag; i > 0; --i)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) at[i][h] = at[i - 1][h];
+            if (j < pc.tiles)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) at[0][h] = find(pc.tile0 + j, h);
+            if (j >= kLag) load(&tmV, at[kLag]);
+            if (j < pc.tiles) load(&tmK, at[0]);
           }
         });
         // outstanding copies must land before the CTA may exit
@@ -420,15 +467,14 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                        kk > 0 ? 1u : 0u);
         }
       };
-      auto issue_pv_half = [&](int t, int sv, int h, bool first) {
+      // O_t += P V over 64 keys: half h of the tile in ring place sv, P from column `p_col` on
+      auto issue_pv_half = [&](int t, uint32_t p_col, int sv, int h, bool first) {
         const uint32_t v_off = (uint32_t)(sv * C::kTile) >> 4;
-        const uint32_t a_tmem = tmem + 128u * t + 64u;
 #pragma unroll
-        for (int k = 0; k < kKeys / 32; ++k) {
-          const int kk = h * (kKeys / 32) + k;
-          umma_ts_warp(tmem + 256u + 128u * t, a_tmem + 8u * kk, dV + v_off + ((kk * 16 * 128) >> 4),
-                       idesc_pv, (!first || kk > 0) ? 1u : 0u);
-        }
+        for (int k = 0; k < kKeys / 32; ++k)
+          umma_ts_warp(tmem + 256u + 128u * t, tmem + p_col + 8u * k,
+                       dV + v_off + (((h * (kKeys / 32) + k) * 16 * 128) >> 4), idesc_pv,
+                       (!first || k > 0) ? 1u : 0u);
       };
       int kv = 0;
       int qloads[2] = {0, 0}, pcount[2] = {0, 0};
@@ -449,21 +495,26 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const int n = pc.tiles;
         // keys of the piece's last tile (all 128 unless it is the sequence's last)
         const int tail = min(pc.s.len - (pc.tile0 + n - 1) * kKeys, kKeys);
-        // PV of tile j for warpgroup t, once its P is there; `last`: t's last of the piece
-        auto pv = [&](int t, int j, bool first, bool last) -> bool {
-          const unsigned iv = (unsigned)(kv + 2 * j + 1);
+        // PV of tile j once its P is there.  Two query tiles: for tile t, in two halves of the
+        // keys as they come.  One: both warpgroups' halves, b the scores' buffer.
+        auto pv = [&](int tb, int j, bool last) -> bool {
+          const int sv = (int)((unsigned)(kv + Order::v(j, n)) % NS);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (!wait(BAR_P + 2 * t + h, pcount[t] & 1, kSiteTreeP)) return false;
+            if (!wait(BAR_P + 2 * tb + h, pcount[tb] & 1, kSiteTreeP)) return false;
             tc_fence_after();
-            issue_pv_half(t, iv % NS, h, first);
+            if constexpr (kTwo)
+              issue_pv_half(tb, 128u * tb + 64u + 32u * h, sv, h, j == 0 && h == 0);
+            else
+              issue_pv_half(h, 128u * tb + 64u * h + 32u, sv, h, j == 0);
           }
-          ++pcount[t];
-          if (last) umma_commit_warp(bar(BAR_O + t));
+          ++pcount[tb];
+          if (!kTwo) umma_commit_warp(bar(BAR_PV + tb));
+          if (last) umma_commit_warp(bar(BAR_O + (kTwo ? tb : 0)));
           return true;
         };
         auto v_ready = [&](int j) -> bool {
-          const unsigned iv = (unsigned)(kv + 2 * j + 1);
+          const unsigned iv = (unsigned)(kv + Order::v(j, n));
           if (!wait(BAR_FULL + iv % NS, (iv / NS) & 1, kSiteTreeFullV)) return false;
           if (tail < kKeys && j == n - 1) {
             // rows past the sequence's end become zeros (a half without any row already is)
@@ -480,13 +531,13 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           return true;
         };
         auto k_ready = [&](int j) -> bool {
-          const unsigned ik = (unsigned)(kv + 2 * j);
+          const unsigned ik = (unsigned)(kv + Order::k(j));
           if (!wait(BAR_FULL + ik % NS, (ik / NS) & 1, kSiteTreeFullK)) return false;
           tc_fence_after();
           return true;
         };
-        auto k_slot = [&](int j) -> int { return (int)((unsigned)(kv + 2 * j) % NS); };
-        auto v_slot = [&](int j) -> int { return (int)((unsigned)(kv + 2 * j + 1) % NS); };
+        auto k_slot = [&](int j) -> int { return (int)((unsigned)(kv + Order::k(j)) % NS); };
+        auto v_slot = [&](int j) -> int { return (int)((unsigned)(kv + Order::v(j, n)) % NS); };
         if constexpr (kTwo) {
           // step j: for each query tile PV of tile j - 1, then QK^T of tile j
           for (int j = 0; j <= n; ++j) {
@@ -495,7 +546,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               if (t == 1 && !used1) continue;
-              if (j > 0 && !pv(t, j - 1, j == 1, j == n)) return;
+              if (j > 0 && !pv(t, j - 1, j == n)) return;
               if (j < n) {
                 issue_qk(t, k_slot(j));
                 umma_commit_warp(bar(BAR_S + t));
@@ -506,14 +557,14 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             if (j < n) umma_commit_warp(bar(BAR_EMPTY + k_slot(j)));
           }
         } else {
-          // step j, warpgroup t = j mod 2: PV of tile j - 2, then QK^T of tile j into the
-          // same scores (the tensor pipe runs in order, so P has been read by then)
+          // step j, scores' buffer t = j mod 2: PV of tile j - 2, then QK^T of tile j into the
+          // same buffer (the tensor pipe runs in order, so P has been read by then)
           for (int j = 0; j < n + 2; ++j) {
             const int t = j & 1;
             if (j < n && !k_ready(j)) return;
             if (j >= 2 && j - 2 < n) {
               if (!v_ready(j - 2)) return;
-              if (!pv(t, j - 2, j - 2 < 2, j >= n)) return;
+              if (!pv(t, j - 2, j == n + 1)) return;
               umma_commit_warp(bar(BAR_EMPTY + v_slot(j - 2)));
             }
             if (j < n) {
@@ -537,7 +588,9 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const int t = warp >> 2, wq = warp & 3;
     const int r = wq * 32 + lane;                         // row of the tile
     const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
-    const uint32_t tS = tmem + lane_off + 128u * t;
+    constexpr int kN = kTwo ? 128 : 64;                   // scores of a tile that a thread takes
+    // this warpgroup's scores (one query tile: of buffer 0, the other is 128 columns on)
+    const uint32_t tS = tmem + lane_off + (kTwo ? 128u : 64u) * t;
     const uint32_t tO = tmem + lane_off + 256u;           // O_0; O_1 is 128 columns on
     float2* ml = reinterpret_cast<float2*>(base + C::kMl);
     // the sequence's parents, a copy a warp: in the 256 bytes that take this warp's own (m, l)
@@ -557,7 +610,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     auto is_row = [&](const Piece& pc, int node) -> bool {
       return r < tile_rows && node < pc.s.nodes;
     };
-    int scount = 0, ocount[2] = {0, 0};      // waits so far for S_t, and for O_0 and O_1
+    int scount = 0, ocount = 0;      // parities of the next waits for scores and for O
     bool ok = true;
 
     for (Run rest = run; rest.count > 0;) {
@@ -597,16 +650,20 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
 
       float m_ref = -INFINITY, l = 0.f;
-      for (int j = kTwo ? 0 : t; j < tiles; j += kTwo ? 1 : 2) {
+      for (int j = 0; j < tiles; ++j) {
+        const int buf = kTwo ? t : j & 1;      // of the scores' barriers
         if (ok) {
-          ok = mbar_wait(bar(BAR_S + t), scount & 1, abort_flag, p.err, kSiteTreeS);
+          ok = mbar_wait(bar(BAR_S + buf), (kTwo ? scount : scount >> buf) & 1, abort_flag, p.err,
+                         kSiteTreeS);
           ok = __all_sync(0xffffffffu, ok);
         }
-        ++scount;
+        // waits so far: their parity, one bit for each buffer where both are waited for
+        scount ^= kTwo ? 1 : 1 << buf;
         if (!ok) continue;
         tc_fence_after();
         if (busy) {
-          uint32_t w[4];      // the keys of a tile that this row's node sees, past the context
+          const uint32_t tSb = kTwo ? tS : tS + 128u * buf;
+          uint32_t w[kN / 32];  // the keys of a tile that this row's node sees, past the context
           if (j >= masked_from) {
             const Piece pc = piece();
             const int node = node_of(pc);
@@ -614,18 +671,20 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             if (p.parents == nullptr) {
               seen = node >= 127 ? ~(unsigned __int128)0 : ((unsigned __int128)1 << (node + 1)) - 1;
             } else {
-              for (int i = is_row(pc, node) ? node : -1; i >= 0; i = par[i]) seen |= (unsigned __int128)1 << i;
+              for (int i = is_row(pc, node) ? node : -1; i >= 0; i = par[i])
+                seen |= (unsigned __int128)1 << i;
             }
             const unsigned __int128 vis =
                 visible_keys(seen, (pc.tile0 + j) * kKeys, pc.s.len - pc.s.n);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = (uint32_t)(vis >> (32 * i));
+            for (int i = 0; i < kN / 32; ++i)
+              w[i] = (uint32_t)(vis >> (32 * i + (kTwo ? 0 : 64 * t)));
           }
-          uint32_t s[128];
-          tmem_ld_x128(tS, s);
+          uint32_t s[kN];
+          tmem_scores(tSb, s);
           if (j >= masked_from) {
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
+            for (int c = 0; c < kN; ++c)
               if (!((w[c >> 5] >> (c & 31)) & 1u)) s[c] = kNegInf;
           }
           const float mx = row_max(s) * p.kscale;
@@ -636,9 +695,17 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             alpha = ex2_approx(m_ref - m_new);
             m_ref = m_new;
           }
-          if (j >= (kTwo ? 1 : 2) && __any_sync(0xffffffffu, need)) {
-            // PV of this warpgroup's previous tile is complete: it was issued before the
-            // product whose commit signalled this S
+          if (j > 0 && __any_sync(0xffffffffu, need)) {
+            // The product of the tile before has to be in O.  Two query tiles: it was issued
+            // before the one whose commit signalled these scores.  One: it comes after, so wait
+            // for its own commit (no later one can follow before this warpgroup's next P).
+            if (!kTwo) {
+              ok = mbar_wait(bar(BAR_PV + (buf ^ 1)), ((scount >> (buf ^ 1)) & 1) ^ 1, abort_flag,
+                             p.err, kSiteTreePv);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) continue;
+              tc_fence_after();
+            }
 #pragma unroll 1
             for (int cc = 0; cc < D / 16; ++cc) {
               uint32_t o[16];
@@ -651,22 +718,26 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
           float sum = 0.f;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
+          for (int half = 0; half < kN / 64; ++half) {
             uint32_t pk[32];
-            sum += row_exp_half(s, 64 * half, p.kscale, m_use, pk);
-            tmem_st_x32(tS + 64u + 32u * half, pk);
+            sum += row_exp_64(s, 64 * half, p.kscale, m_use, pk);
+            tmem_st_x32(kTwo ? tSb + 64u + 32u * half : tSb + 32u, pk);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(BAR_P + 2 * t + half));
+            if (lane == 0) mbar_arrive(bar(BAR_P + 2 * buf + (kTwo ? half : t)));
           }
           l = l * alpha + sum;
         } else {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(bar(BAR_P + 2 * t));
-            mbar_arrive(bar(BAR_P + 2 * t + 1));
+            if (kTwo) {
+              mbar_arrive(bar(BAR_P + 2 * buf));
+              mbar_arrive(bar(BAR_P + 2 * buf + 1));
+            } else {
+              mbar_arrive(bar(BAR_P + 2 * buf + t));
+            }
           }
         }
       }
@@ -679,11 +750,6 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       constexpr int kCols = kTwo ? D : D / 2;         // columns this thread writes
       const int col0 = kTwo ? 0 : t * (D / 2);
       if constexpr (kTwo) {
-        if (ok) {
-          ok = mbar_wait(bar(BAR_O + t), ocount[0] & 1, abort_flag, p.err, kSiteTreeO);
-          ok = __all_sync(0xffffffffu, ok);
-        }
-        ++ocount[0];
         f0 = 1.f;
       } else {
         // (m, l) cross through shared memory; both O's are in this row's TMEM lane
@@ -693,16 +759,14 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         m = fmaxf(a.x, b.x);
         const float mu = m == -INFINITY ? 0.f : m;
         f0 = ex2_approx(a.x - mu);
-        f1 = pc.tiles > 1 ? ex2_approx(b.x - mu) : 0.f;
+        f1 = ex2_approx(b.x - mu);
         lsum = a.y * f0 + b.y * f1;
-        for (int q = 0; q < 2 && q < pc.tiles; ++q) {
-          if (ok) {
-            ok = mbar_wait(bar(BAR_O + q), ocount[q] & 1, abort_flag, p.err, kSiteTreeO);
-            ok = __all_sync(0xffffffffu, ok);
-          }
-          ++ocount[q];
-        }
       }
+      if (ok) {
+        ok = mbar_wait(bar(BAR_O + (kTwo ? t : 0)), ocount & 1, abort_flag, p.err, kSiteTreeO);
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      ocount ^= 1;
       if (ok && busy) {
         tc_fence_after();
         const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
@@ -722,7 +786,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           tmem_ld_x16(src + 16u * cc, a);
 #pragma unroll
           for (int k = 0; k < 16; ++k) v[k] = fl(a[k]) * g0;
-          if (!kTwo && pc.tiles > 1) {
+          if (!kTwo) {
             tmem_ld_x16(src + 128u + 16u * cc, a);
 #pragma unroll
             for (int k = 0; k < 16; ++k) v[k] = fmaf(fl(a[k]), g1, v[k]);
@@ -776,6 +840,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 // end like the stores that left the pieces, and its own stores whole sectors.  The pieces of a
 // segment lie with consecutive CTAs; rows of a segment in one piece are already written.
 constexpr int kJoinCols = 16;
+constexpr int kJoinPieces = 4;
 
 template <int D>
 __global__ void __launch_bounds__(256) attn_tree_join_kernel(const TreeParams p, int tiles) {
@@ -809,24 +874,42 @@ __global__ void __launch_bounds__(256) attn_tree_join_kernel(const TreeParams p,
   const int c1 = (int)((u1 * parts - 1) / total);
   if (c0 == c1) return;
   auto part = [&](int c) -> size_t { return (size_t)(2 * c + (c == c0 ? 1 : 0)) * tiles + tile; };
-  float m = -INFINITY;
-  for (int c = c0; c <= c1; ++c) m = fmaxf(m, p.ml_part[part(c) * kTreeRows + r].x);
-  float acc[kJoinCols] = {}, l = 0.f;
-  if (m != -INFINITY) {
-    for (int c = c0; c <= c1; ++c) {
-      const float2 a = p.ml_part[part(c) * kTreeRows + r];
-      if (a.x == -INFINITY) continue;
-      const float w = ex2_approx(a.x - m);
-      l = fmaf(w, a.y, l);
-      const float4* src = reinterpret_cast<const float4*>(p.o_part) +
-                          part(c) * (D / 4 * kTreeRows) + col / 4 * kTreeRows + r;
+  // kJoinPieces pieces at a time, their loads issued together: most rows have no more
+  float m = -INFINITY, l = 0.f, acc[kJoinCols] = {};
+  for (int c = c0; c <= c1; c += kJoinPieces) {
+    float2 a[kJoinPieces];
+    float4 v[kJoinPieces][kJoinCols / 4];
+#pragma unroll
+    for (int i = 0; i < kJoinPieces; ++i) {
+      a[i] = make_float2(-INFINITY, 0.f);
+      if (c + i > c1) continue;
+      const size_t at = part(c + i);
+      a[i] = p.ml_part[at * kTreeRows + r];
+      const float4* src = reinterpret_cast<const float4*>(p.o_part) + at * (D / 4 * kTreeRows) +
+                          col / 4 * kTreeRows + r;
+#pragma unroll
+      for (int k = 0; k < kJoinCols / 4; ++k) v[i][k] = src[k * kTreeRows];
+    }
+    float mn = m;
+#pragma unroll
+    for (int i = 0; i < kJoinPieces; ++i) mn = fmaxf(mn, a[i].x);
+    if (mn == -INFINITY) continue;
+    const float old = ex2_approx(m - mn);
+    m = mn;
+    l *= old;
+#pragma unroll
+    for (int k = 0; k < kJoinCols; ++k) acc[k] *= old;
+#pragma unroll
+    for (int i = 0; i < kJoinPieces; ++i) {
+      if (a[i].x == -INFINITY) continue;      // no piece, or one without a key for this row
+      const float w = ex2_approx(a[i].x - m);
+      l = fmaf(w, a[i].y, l);
 #pragma unroll
       for (int k = 0; k < kJoinCols / 4; ++k) {
-        const float4 v = src[k * kTreeRows];
-        acc[4 * k] = fmaf(w, v.x, acc[4 * k]);
-        acc[4 * k + 1] = fmaf(w, v.y, acc[4 * k + 1]);
-        acc[4 * k + 2] = fmaf(w, v.z, acc[4 * k + 2]);
-        acc[4 * k + 3] = fmaf(w, v.w, acc[4 * k + 3]);
+        acc[4 * k] = fmaf(w, v[i][k].x, acc[4 * k]);
+        acc[4 * k + 1] = fmaf(w, v[i][k].y, acc[4 * k + 1]);
+        acc[4 * k + 2] = fmaf(w, v[i][k].z, acc[4 * k + 2]);
+        acc[4 * k + 3] = fmaf(w, v[i][k].w, acc[4 * k + 3]);
       }
     }
   }
