@@ -294,11 +294,11 @@ ATTN_API int attn_decode_merge(const float* o_part, const float* lse_part, void*
  *   c = ctx_lens[b] clamped to [0, cap]         rows in the cache before the step
  *   token_offsets[b] = min(sum of max(new_lens, 0) before b, num_tokens); n = their difference
  *   seq_lens[b] = min(c + n, cap)
- *   pages: the sequence owns ceil(c / page_size) table entries and takes
- *     ceil(seq_lens[b] / page_size) - that many more, the next entries of free_pages after
- *     free_used[0] (0 if free_used is NULL) and after the sequences before b; they are written
- *     to its block-table row, -1 where the free list has ended.  The other entries of the row
- *     stay as they are.
+ *   pages: the sequence owns the first ceil(max(c, held_rows[b]) / page_size) entries of its
+ *     block-table row (held_rows NULL: of c) and takes as many more as seq_lens[b] rows need,
+ *     the next entries of free_pages after free_used[0] (0 if free_used is NULL) and after the
+ *     sequences before b; they are written to the row, -1 where the free list has ended.  The
+ *     other entries stay as they are.
  *   token i of b goes to row c + i:  slots = page * page_size + (c + i) mod page_size, -1 for
  *     a row past cap or without a page; positions = c + i, or with parents (a drafted tree,
  *     see attn_decode_tree) c + depth, a node without a parent having depth 0.
@@ -308,6 +308,9 @@ ATTN_API int attn_decode_merge(const float* o_part, const float* lse_part, void*
  *
  *   ctx_lens, new_lens  int32 [B]           free_pages  int32 [num_free]
  *   free_used   int32 [1] or NULL           parents     int32 [num_tokens] or NULL
+ *   held_rows   int32 [B] or NULL: rows for which pages were taken before, where these are more
+ *               than ctx_lens (drafted tokens that were rejected leave such rows); the largest
+ *               seq_lens of the steps so far.  Without it their pages are taken anew.
  *   block_table int32 [B, max_pages_per_seq] (updated)
  *   slots       int64 [num_tokens], positions int32 [num_tokens]   (written; 16-byte aligned,
  *               the int32 arrays 4-byte aligned)
@@ -319,10 +322,10 @@ ATTN_API int attn_decode_merge(const float* o_part, const float* lse_part, void*
  * Errors: INVALID_ARG, UNSUPPORTED (B > 16384; cap >= 2^31), MISALIGNED, CUDA.
  */
 ATTN_API int attn_page_tables(const int* ctx_lens, const int* new_lens, const int* free_pages,
-             const int* free_used, const int* parents, int* block_table, long long* slots,
-             int* positions, int* seq_lens, int* token_offsets, int* pages_used, int B,
-             int max_pages_per_seq, int page_size, int num_free, int num_tokens,
-             cudaStream_t stream);
+             const int* free_used, const int* held_rows, const int* parents, int* block_table,
+             long long* slots, int* positions, int* seq_lens, int* token_offsets,
+             int* pages_used, int B, int max_pages_per_seq, int page_size, int num_free,
+             int num_tokens, cudaStream_t stream);
 
 /*
  * attn_qk_norm_rope -- from the projection's output to the inputs of attn_fwd in one pass:
@@ -342,7 +345,8 @@ ATTN_API int attn_page_tables(const int* ctx_lens, const int* new_lens, const in
  *            [0, table_rows) reads a table row of zeros.
  *   interleaved 0: pair i is (i, i + rot / 2); else (2 i, 2 i + 1)
  *   eps      positive and normal in fp32 (with a norm)
- * Statistics and products are fp32, outputs rounded once.
+ * Statistics and products are fp32, outputs rounded once.  An output may not overlap an input
+ * or another output (INVALID_ARG).
  * Errors: INVALID_ARG, UNSUPPORTED (d; rot; more than 4096 heads), MISALIGNED, CUDA.
  */
 ATTN_API int attn_qk_norm_rope(const void* qkv, const void* q_weight, const void* k_weight,
@@ -414,7 +418,8 @@ ATTN_API int attn_qk_norm_rope_paged(const void* qkv, const void* q_weight, cons
  * LSE = -inf.  What a page holds past the sequence's end is not used, whatever it is; rows
  * inside the length take part in one product for all nodes of the sequence, so a NaN or
  * infinity in V there may reach nodes that do not see its row.
- * Hq / Hkv <= 16, d in {64, 128}, page_size a multiple of 64.
+ * Hq / Hkv <= 16, d in {64, 128}, page_size a multiple of 64.  o, lse and the workspace may not
+ * overlap an input or each other (INVALID_ARG).
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, CUDA.
  */
 ATTN_API size_t attn_decode_tree_workspace_bytes(int B, int Hq, int Hkv, int max_nodes, int d,

@@ -52,7 +52,7 @@ SIGNATURES = {
                                             c_void_p]),
     "attn_decode_merge": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_longlong, c_int,
                                   c_int, c_void_p]),
-    "attn_page_tables": (c_int, [c_void_p] * 11 + [c_int] * 5 + [c_void_p]),
+    "attn_page_tables": (c_int, [c_void_p] * 12 + [c_int] * 5 + [c_void_p]),
     "attn_qk_norm_rope": (c_int, [c_void_p] * 8 + [c_int] * 7 + [c_float, c_int, c_void_p]),
     "attn_qk_norm_rope_bwd_workspace_bytes": (c_size_t, [c_int]),
     "attn_qk_norm_rope_bwd": (c_int, [c_void_p] * 11 + [c_int] * 7

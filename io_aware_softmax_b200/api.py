@@ -465,6 +465,7 @@ def _result(t, name: str, dtype: torch.dtype, shape, ref: torch.Tensor) -> torch
 def attn_page_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor,
                      block_table: torch.Tensor, *, page_size: int, num_tokens: int,
                      free_used: Optional[torch.Tensor] = None,
+                     held_rows: Optional[torch.Tensor] = None,
                      parents: Optional[torch.Tensor] = None,
                      slots: Optional[torch.Tensor] = None,
                      positions: Optional[torch.Tensor] = None,
@@ -477,7 +478,8 @@ def attn_page_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages:
     Returns (slots int64 [num_tokens], positions int32 [num_tokens], seq_lens int32 [B],
     token_offsets int32 [B+1], pages_used int32 [1]).  ``parents`` (int32 [num_tokens]) gives
     the tokens of drafted trees positions by depth; ``free_used`` is the pages_used of an
-    earlier step on the same free list."""
+    earlier step on the same free list; ``held_rows`` (int32 [B]) are the rows that already
+    have pages, where rejected drafts made them more than ctx_lens."""
     lib = _lib.load()
     i32 = torch.int32
     _need(ctx_lens, "ctx_lens", i32, 1)
@@ -490,6 +492,7 @@ def attn_page_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages:
     _given(block_table, "block_table", i32, (B, max_pages), ctx_lens)
     _given(new_lens, "new_lens", i32, (B,), ctx_lens)
     _optional(free_used, "free_used", i32, (1,), ctx_lens)
+    _optional(held_rows, "held_rows", i32, (B,), ctx_lens)
     _optional(parents, "parents", i32, (T,), ctx_lens)
     slots = _result(slots, "slots", torch.int64, (T,), ctx_lens)
     if positions is seq_lens is token_offsets is pages_used is None:
@@ -506,9 +509,9 @@ def attn_page_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages:
         pages_used = _result(pages_used, "pages_used", i32, (1,), ctx_lens)
     with _device(ctx_lens):
         st = lib.attn_page_tables(_ptr(ctx_lens), _ptr(new_lens), _ptr(free_pages),
-                                  _ptr(free_used), _ptr(parents), _ptr(block_table), _ptr(slots),
-                                  _ptr(positions), _ptr(seq_lens), _ptr(token_offsets),
-                                  _ptr(pages_used), B, max_pages, int(page_size),
+                                  _ptr(free_used), _ptr(held_rows), _ptr(parents),
+                                  _ptr(block_table), _ptr(slots), _ptr(positions),
+                                  _ptr(seq_lens), _ptr(token_offsets), _ptr(pages_used), B, max_pages, int(page_size),
                                   num_free, T, _stream(ctx_lens.device, stream))
     _check(st, "attn_page_tables")
     return slots, positions, seq_lens, token_offsets, pages_used

@@ -642,14 +642,37 @@ extern "C" int attn_fwd_fp8(const void* q8, const void* k8, const void* vt8,
 
 // ------------------------------------------------------------------ page tables and slots
 
-static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a != nullptr && b != nullptr && na > 0 && nb > 0 && x < y + nb && y < x + na;
+namespace {
+
+// Bytes that a call reads or writes (a null pointer: none).
+struct Range {
+  const void* ptr;
+  size_t bytes;
+};
+
+bool overlap(const Range& a, const Range& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.ptr), y = reinterpret_cast<uintptr_t>(b.ptr);
+  return a.ptr != nullptr && b.ptr != nullptr && a.bytes > 0 && b.bytes > 0 &&
+         x < y + b.bytes && y < x + a.bytes;
 }
 
+// Whether an output lies on an input or on another output: blocks read while others write.
+template <size_t I, size_t O>
+bool overlaps(const Range (&ins)[I], const Range (&outs)[O]) {
+  for (size_t o = 0; o < O; ++o) {
+    for (size_t i = 0; i < I; ++i)
+      if (overlap(ins[i], outs[o])) return true;
+    for (size_t i = 0; i < o; ++i)
+      if (overlap(outs[i], outs[o])) return true;
+  }
+  return false;
+}
+
+}  // namespace
+
 extern "C" int attn_page_tables(const int* ctx_lens, const int* new_lens, const int* free_pages,
-                                const int* free_used, const int* parents, int* block_table,
-                                long long* slots, int* positions, int* seq_lens,
+                                const int* free_used, const int* held_rows, const int* parents,
+                                int* block_table, long long* slots, int* positions, int* seq_lens,
                                 int* token_offsets, int* pages_used, int B, int max_pages_per_seq,
                                 int page_size, int num_free, int num_tokens,
                                 cudaStream_t stream) {
@@ -665,23 +688,18 @@ extern "C" int attn_page_tables(const int* ctx_lens, const int* new_lens, const 
   const void* ptrs[] = {slots, positions};
   for (const void* q : ptrs)
     if (!aligned16(q)) return ATTN_ERR_MISALIGNED;
-  const void* ints[] = {ctx_lens, new_lens, free_pages, free_used, parents,
-                        block_table, seq_lens, token_offsets, pages_used};
+  const void* ints[] = {ctx_lens,  new_lens,    free_pages, free_used,     held_rows,
+                        parents,   block_table, seq_lens,   token_offsets, pages_used};
   for (const void* q : ints)
     if (reinterpret_cast<uintptr_t>(q) & 3u) return ATTN_ERR_MISALIGNED;
   // every block reads the inputs while block 0 writes the outputs
   const size_t nb = (size_t)B * 4, nt = (size_t)num_tokens * 4;
-  const void* ins[] = {ctx_lens, new_lens, free_pages, free_used, parents};
-  const size_t in_bytes[] = {nb, nb, (size_t)num_free * 4, 4, nt};
-  const void* outs[] = {block_table, slots, positions, seq_lens, token_offsets, pages_used};
-  const size_t out_bytes[] = {nb * max_pages_per_seq, 2 * nt, nt, nb, nb + 4, 4};
-  for (int o = 0; o < 6; ++o) {
-    for (int i = 0; i < 5; ++i)
-      if (overlap(ins[i], in_bytes[i], outs[o], out_bytes[o])) return ATTN_ERR_INVALID_ARG;
-    for (int i = 0; i < o; ++i)
-      if (overlap(outs[i], out_bytes[i], outs[o], out_bytes[o])) return ATTN_ERR_INVALID_ARG;
-  }
-  PagesParams p{ctx_lens, new_lens, free_pages, free_used, parents, block_table, slots, positions,
+  const Range ins[] = {{ctx_lens, nb}, {new_lens, nb}, {free_pages, (size_t)num_free * 4},
+                       {free_used, 4}, {held_rows, nb}, {parents, nt}};
+  const Range outs[] = {{block_table, nb * max_pages_per_seq}, {slots, 2 * nt}, {positions, nt},
+                        {seq_lens, nb}, {token_offsets, nb + 4}, {pages_used, 4}};
+  if (overlaps(ins, outs)) return ATTN_ERR_INVALID_ARG;
+  PagesParams p{ctx_lens, new_lens, free_pages, free_used, held_rows, parents, block_table, slots, positions,
                 seq_lens, token_offsets, pages_used, B, max_pages_per_seq, page_size, num_free,
                 num_tokens};
   return launch_page_tables(p, sm_count(current_device()), stream) == 0 ? ATTN_OK : ATTN_ERR_CUDA;
@@ -740,6 +758,12 @@ extern "C" int attn_qk_norm_rope(const void* qkv, const void* q_weight, const vo
   if (p.tokens == 0 || p.H == 0) return ATTN_OK;
   if ((Hq > 0 && !q) || (Hkv > 0 && (!k || !v))) return ATTN_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v)) return ATTN_ERR_MISALIGNED;
+  const size_t head = (size_t)p.tokens * d * 2;
+  const Range ins[] = {{qkv, head * p.H}, {q_weight, (size_t)d * 2}, {k_weight, (size_t)d * 2},
+                       {rope_table, (size_t)table_rows * rot * 4},
+                       {positions, (size_t)p.tokens * 4}};
+  const Range outs[] = {{q, head * Hq}, {k, head * Hkv}, {v, head * Hkv}};
+  if (overlaps(ins, outs)) return ATTN_ERR_INVALID_ARG;
   p.q = q;
   p.k = k;
   p.v = v;
@@ -764,6 +788,12 @@ extern "C" int attn_qk_norm_rope_paged(const void* qkv, const void* q_weight,
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) ||
       (reinterpret_cast<uintptr_t>(slots) & 7u))
     return ATTN_ERR_MISALIGNED;
+  const size_t head = (size_t)T * d * 2, cache = (size_t)num_pages * page_size * Hkv * d * 2;
+  const Range ins[] = {{qkv, head * p.H}, {q_weight, (size_t)d * 2}, {k_weight, (size_t)d * 2},
+                       {rope_table, (size_t)table_rows * rot * 4}, {positions, (size_t)T * 4},
+                       {slots, (size_t)T * 8}};
+  const Range outs[] = {{q, head * Hq}, {k_pages, cache}, {v_pages, cache}};
+  if (overlaps(ins, outs)) return ATTN_ERR_INVALID_ARG;
   p.q = q;
   p.k = k_pages;
   p.v = v_pages;
@@ -809,6 +839,15 @@ extern "C" int attn_qk_norm_rope_bwd(const void* qkv, const void* q_weight, cons
       return ATTN_ERR_WORKSPACE;
     if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
   }
+  const size_t head = (size_t)p.f.tokens * d * 2, gain = (size_t)d * 4;
+  const Range ins[] = {{qkv, head * p.f.H}, {q_weight, gain / 2}, {k_weight, gain / 2},
+                       {rope_table, (size_t)table_rows * rot * 4},
+                       {positions, (size_t)p.f.tokens * 4}, {dq, head * Hq}, {dk, head * Hkv},
+                       {dv, head * Hkv}};
+  const Range outs[] = {{dqkv, head * p.f.H}, {norm ? dq_weight : nullptr, gain},
+                        {norm ? dk_weight : nullptr, gain},
+                        {norm ? workspace : nullptr, attn_qk_norm_rope_bwd_workspace_bytes(d)}};
+  if (overlaps(ins, outs)) return ATTN_ERR_INVALID_ARG;
   p.f.q = const_cast<void*>(dq);
   p.f.k = const_cast<void*>(dk);
   p.f.v = const_cast<void*>(dv);
@@ -888,6 +927,12 @@ extern "C" int attn_decode_tree(const void* q, const void* k_pages, const void* 
     return ATTN_ERR_UNSUPPORTED;
   if (workspace == nullptr || workspace_bytes < plan.bytes) return ATTN_ERR_WORKSPACE;
   if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
+  const size_t row = (size_t)T * Hq, cache = (size_t)num_pages * page_size * Hkv * d * 2;
+  const Range ins[] = {{q, row * d * 2}, {k_pages, cache}, {v_pages, cache},
+                       {block_table, (size_t)B * max_pages_per_seq * 4}, {seq_lens, (size_t)B * 4},
+                       {token_offsets, (size_t)B * 4 + 4}, {parents, (size_t)T * 4}};
+  const Range outs[] = {{o, row * d * 2}, {lse, row * 4}, {workspace, plan.bytes}};
+  if (overlaps(ins, outs)) return ATTN_ERR_INVALID_ARG;
   if (scale <= 0.f) scale = 1.0f / std::sqrt((float)d);
 
   TreeParams p{};

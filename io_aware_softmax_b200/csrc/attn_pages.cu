@@ -1,9 +1,10 @@
 // Block tables and slot maps of a paged cache from request lengths, on the GPU.
 //
 // Sequence b holds c = ctx_lens[b] cache rows and adds n = new_lens[b] tokens.  With page size
-// P it owns ceil(c / P) pages and takes ceil((c + n) / P) - ceil(c / P) more, which come off
-// the free list in sequence order; token i of the sequence lands in row c + i.  Everything
-// follows from two prefix sums over the sequences, of tokens and of taken pages.
+// P it owns ceil(c / P) pages, or more where rows behind c were taken back (held_rows), and
+// takes what ceil((c + n) / P) exceeds them by; these come off the free list in sequence order.
+// Token i of the sequence lands in row c + i.  Everything follows from two prefix sums over
+// the sequences, of tokens and of taken pages.
 //
 // The bytes (12 a token, 8 a new page) take microseconds at most, so the launch and the
 // latencies on the way to the first store are the cost.  One launch does all: every block
@@ -76,6 +77,10 @@ __global__ void __launch_bounds__(kPagesThreads) attn_page_tables_kernel(const P
     return (int)(((unsigned long long)(unsigned)row * p.div_mul) >> p.div_shift);
   };
   auto pages_of = [&](int rows) -> int { return rows > 0 ? page_of(rows - 1) + 1 : 0; };
+  // pages that sequence b owns before the step, with c rows held
+  auto owned = [&](int b, int c) -> int {
+    return pages_of(p.held_rows != nullptr ? min(max(__ldg(p.held_rows + b), c), cap) : c);
+  };
   auto grown = [&](int c, long long n) -> int {
     return (int)min((long long)c + n, (long long)cap);
   };
@@ -85,7 +90,7 @@ __global__ void __launch_bounds__(kPagesThreads) attn_page_tables_kernel(const P
     const int c = min(max(__ldg(p.ctx_lens + b), 0), cap), n = max(__ldg(p.new_lens + b), 0);
     held[b] = c;
     mine.tokens += n;
-    mine.pages += pages_of(grown(c, n)) - pages_of(c);
+    mine.pages += max(pages_of(grown(c, n)) - owned(b, c), 0);
   }
   const long long used0 = p.free_used != nullptr ? max(__ldg(p.free_used), 0) : 0;
   Sums run = block_scan(mine, warp_sums[0], total);
@@ -96,7 +101,8 @@ __global__ void __launch_bounds__(kPagesThreads) attn_page_tables_kernel(const P
     for (int b = b0; b < b1; ++b) {
       const int n = max(__ldg(p.new_lens + b), 0);
       const long long room = max((long long)p.num_tokens - t, 0LL);
-      mine.pages += pages_of(grown(held[b], min((long long)n, room))) - pages_of(held[b]);
+      const int e = grown(held[b], min((long long)n, room));
+      mine.pages += max(pages_of(e) - owned(b, held[b]), 0);
       t += n;
     }
     run = block_scan(mine, warp_sums[1], total);
@@ -111,7 +117,7 @@ __global__ void __launch_bounds__(kPagesThreads) attn_page_tables_kernel(const P
     const int e = grown(held[b], end - o);
     off[b] = o;
     first[b] = (int)min(run.pages, (long long)INT_MAX);
-    run.pages += pages_of(e) - pages_of(held[b]);
+    run.pages += max(pages_of(e) - owned(b, held[b]), 0);
     if (blockIdx.x == 0) {
       p.seq_lens[b] = e;
       p.token_offsets[b] = o;
@@ -164,7 +170,7 @@ __global__ void __launch_bounds__(kPagesThreads) attn_page_tables_kernel(const P
       if (row < cap) {
         const int pg = page_of((int)row);
         if (pg != known) {
-          const int have = pages_of(c);
+          const int have = owned(b, c);
           known = pg;
           page = pg < have ? p.block_table[(size_t)b * p.max_pages + pg] : free_page(b, pg - have);
         }
@@ -201,7 +207,7 @@ __global__ void __launch_bounds__(kPagesThreads) attn_page_tables_kernel(const P
   // new table entries: a warp for each sequence
   const int lane = tid & 31;
   for (int b = blockIdx.x * kPagesWarps + (tid >> 5); b < p.B; b += gridDim.x * kPagesWarps) {
-    const int c = held[b], have = pages_of(c);
+    const int c = held[b], have = owned(b, c);
     const int need = pages_of(grown(c, off[b + 1] - off[b])) - have;
     int* row = p.block_table + (size_t)b * p.max_pages + have;
     for (int j = lane; j < need; j += 32) row[j] = free_page(b, j);

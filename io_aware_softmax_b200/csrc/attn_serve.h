@@ -33,6 +33,7 @@ struct PagesParams {
   const int* new_lens;      // [B]
   const int* free_pages;    // [num_free]
   const int* free_used;     // [1] or null
+  const int* held_rows;     // [B] or null
   const int* parents;       // [num_tokens] or null
   int* block_table;         // [B, max_pages] (new entries written)
   long long* slots;         // [num_tokens] (written)

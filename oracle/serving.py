@@ -25,7 +25,7 @@ def tree_depth(parents, i: int) -> int:
 
 
 def page_tables(ctx_lens, new_lens, free_pages, block_table, page_size: int, num_tokens: int,
-                free_used: int = 0, parents=None):
+                free_used: int = 0, parents=None, held_rows=None):
     """(slots, positions, seq_lens, token_offsets, pages_used, block_table) of one step."""
     table = np.array(block_table, dtype=np.int32)
     B, P = table.shape
@@ -38,7 +38,8 @@ def page_tables(ctx_lens, new_lens, free_pages, block_table, page_size: int, num
         o = offsets[-1]
         n = min(max(int(new_lens[b]), 0), num_tokens - o)
         end = min(c + n, cap)
-        for p in range(-(-c // page_size), -(-end // page_size)):
+        owned = c if held_rows is None else min(max(int(held_rows[b]), c), cap)
+        for p in range(-(-owned // page_size), -(-end // page_size)):
             table[b, p] = free_pages[used] if used < len(free_pages) else -1
             used += 1
         mine = None if parents is None else parents[o:o + n]

@@ -19,10 +19,11 @@ import torch
 import oracle
 import workloads
 from io_aware_softmax_b200 import (attn_bwd, attn_decode_paged, attn_decode_tree,
-                                   attn_decode_tree_workspace_bytes, attn_fwd, attn_page_tables,
+                                   attn_decode_tree_workspace_bytes, attn_fwd,
+                                   attn_last_error_site, attn_page_tables,
                                    attn_qk_norm_rope, attn_qk_norm_rope_bwd,
                                    attn_qk_norm_rope_bwd_workspace_bytes, attn_qk_norm_rope_paged,
-                                   device_status)
+                                   attn_set_wait_limit_ns, device_status)
 from tests.gpu_common import f64
 
 pytestmark = pytest.mark.gpu
@@ -49,13 +50,14 @@ def within(got, want, bound, what):
 
 # ------------------------------------------------------------------------- page tables
 
-def check_tables(ctx, new, pool, table, page, T, used=None, parents=None):
+def check_tables(ctx, new, pool, table, page, T, used=None, parents=None, held=None):
     got = attn_page_tables(i32(ctx), i32(new), i32(pool), t := i32(table).reshape(len(ctx), -1),
                            page_size=page, num_tokens=T,
                            free_used=None if used is None else i32([used]),
-                           parents=None if parents is None else i32(parents))
+                           parents=None if parents is None else i32(parents),
+                           held_rows=None if held is None else i32(held))
     want = oracle.page_tables(ctx, new, pool, np.reshape(table, (len(ctx), -1)), page, T,
-                              used or 0, parents)
+                              used or 0, parents, held)
     for g, w, name in zip((*got, t), want,
                           ("slots", "positions", "seq_lens", "offsets", "used", "table")):
         assert np.array_equal(g.cpu().numpy(), w), (name, g.cpu().numpy(), w)
@@ -73,6 +75,9 @@ def test_page_tables_random(page, B):
     total = int(np.maximum(new, 0).sum())
     for T in (total, total + 13, max(total - 5, 0)):
         check_tables(ctx.tolist(), new.tolist(), pool.tolist(), table.tolist(), page, T)
+    held = ctx + rng.integers(-3, 2 * page + 2, B)
+    check_tables(ctx.tolist(), new.tolist(), pool.tolist(), table.tolist(), page, total,
+                 held=held.tolist())
 
 
 def test_page_tables_edges():
@@ -623,6 +628,27 @@ def test_two_streams_at_once():
         for n in a:
             if n != "ws":
                 assert torch.equal(a[n], b[n]), n
+
+
+@pytest.mark.parametrize("nodes", [9, 40])
+def test_a_wait_that_runs_out_is_reported_and_later_calls_run(nodes):
+    # caches long enough that every CTA waits for many copies from memory: the device timer
+    # advances in steps of up to a microsecond, and only a wait that sees it move runs out
+    lens, n = [60000, 45000, 20], [nodes, 7, 3]
+    q, kp, vp, table, offsets, par = tree_inputs(lens, n, 16, 4, 128, 64, 90)
+    args = (q, kp, vp, i32(table), i32(lens), i32(offsets))
+    want = attn_decode_tree(*args, max_nodes=nodes, parents=i32(par))
+    assert device_status() == 0
+    attn_set_wait_limit_ns(1)
+    try:
+        attn_decode_tree(*args, max_nodes=nodes, parents=i32(par))
+        assert device_status() == -5
+        assert attn_last_error_site() > 200
+    finally:
+        attn_set_wait_limit_ns(0)
+    again = attn_decode_tree(*args, max_nodes=nodes, parents=i32(par))
+    assert device_status() == 0
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
 
 
 def test_empty_calls():

@@ -36,6 +36,20 @@ def test_page_tables_pool_runs_out_and_tokens_past_the_capacity_have_no_place():
     assert off.tolist() == [0, 6, 8] and lens.tolist() == [6, 2] and used.tolist() == [4]
 
 
+def test_page_tables_keeps_the_pages_of_rejected_rows():
+    # 6 rows, then 4 drafted of which none was accepted: the second page is there already
+    args = dict(page_size=4, num_tokens=5)
+    _, _, lens, _, used, table = oracle.page_tables([3], [5], [7, 8], [[6, 0, 0]], **args)
+    assert table.tolist() == [[6, 7, 0]] and lens.tolist() == [8] and used.tolist() == [1]
+    slots, _, _, _, used, table = oracle.page_tables([3], [5], [7, 8], table, free_used=1,
+                                                     held_rows=lens, **args)
+    assert table.tolist() == [[6, 7, 0]] and used.tolist() == [1]
+    assert slots.tolist() == [27, 28, 29, 30, 31]
+    # more than the table has, or less than the rows
+    assert oracle.page_tables([3], [5], [9], table, held_rows=[99], **args)[4].tolist() == [0]
+    assert oracle.page_tables([3], [5], [9], table, held_rows=[-1], **args)[5].tolist() == [[6, 9, 0]]
+
+
 def test_tree_depth_and_bad_parents():
     parents = [-1, 0, 0, 1, 9, 5, -7]        # 4: not an earlier node, 5: itself
     assert [oracle.tree_depth(parents, i) for i in range(7)] == [0, 1, 1, 2, 0, 0, 0]
@@ -151,7 +165,7 @@ def test_calls_go_through_with_the_sizes(lib):
                                page_size=64, num_tokens=11, parents=z((11,), I32),
                                free_used=z((1,), I32))
     assert [tuple(t.shape) for t in out] == [(11,), (11,), (3,), (4,), (1,)]
-    assert only_call(lib, "attn_page_tables")[11:16] == (3, 7, 64, 9, 11)
+    assert only_call(lib, "attn_page_tables")[12:17] == (3, 7, 64, 9, 11)
     lib.calls.clear()
     q, k, v = api.attn_qk_norm_rope(z((2, 5, 8, 64)), z((64,)), z((64,)), z((5, 32), F32),
                                     num_q_heads=4)
@@ -175,7 +189,8 @@ def test_calls_go_through_with_the_sizes(lib):
 
 @pytest.mark.parametrize("change", [
     dict(new_lens=z((2,), I32)), dict(new_lens=z((3,), I64)), dict(block_table=z((2, 7), I32)),
-    dict(parents=z((10,), I32)), dict(free_used=z((2,), I32)), dict(slots=z((11,), I32)),
+    dict(parents=z((10,), I32)), dict(free_used=z((2,), I32)), dict(held_rows=z((2,), I32)),
+    dict(slots=z((11,), I32)),
     dict(positions=z((12,), I32)), dict(seq_lens=z((4,), I32)), dict(token_offsets=z((3,), I32)),
     dict(pages_used=z((), I32)), dict(num_tokens=-1), dict(ctx_lens=z((6,), I32)[::2]),
     dict(free_pages=z((9,), I32, device="meta"))])
@@ -254,8 +269,8 @@ def clib():
     return _lib.load()
 
 
-def at(k):
-    return ctypes.c_void_p(k << 12)
+def at(k, off=0):
+    return ctypes.c_void_p((k << 24) + off)
 
 
 def call(fn, args, **change):
@@ -263,21 +278,21 @@ def call(fn, args, **change):
 
 
 def test_page_tables_status(clib):
-    a = dict(ctx=at(1), new=at(2), free=at(3), used=at(4), parents=None, table=at(5), slots=at(6),
+    a = dict(ctx=at(1), new=at(2), free=at(3), used=at(4), held=at(12), parents=None, table=at(5), slots=at(6),
              pos=at(7), lens=at(8), off=at(9), out=at(10), B=3, P=7, ps=64, nf=9, T=11, stream=None)
     f = clib.attn_page_tables
     for change in (dict(B=-1), dict(P=-1), dict(ps=0), dict(nf=-1), dict(T=-1), dict(ctx=None),
                    dict(new=None), dict(free=None), dict(table=None), dict(slots=None),
                    dict(lens=None), dict(off=None), dict(out=None),
                    # an output on an input, and two outputs on each other
-                   dict(lens=at(1)), dict(out=at(4)), dict(slots=at(7)),
-                   dict(off=ctypes.c_void_p((8 << 12) + 8))):
+                   dict(lens=at(1)), dict(out=at(4)), dict(slots=at(7)), dict(lens=at(12, -4)),
+                   dict(off=at(8, 8))):
         assert call(f, a, **change) == -1, change
     assert call(f, a, B=16385) == -2
     assert call(f, a, P=1 << 20, ps=4096) == -2
-    assert call(f, a, slots=ctypes.c_void_p((6 << 12) + 8)) == -3
-    assert call(f, a, pos=ctypes.c_void_p((7 << 12) + 4)) == -3
-    assert call(f, a, parents=ctypes.c_void_p((11 << 12) + 2)) == -3
+    assert call(f, a, slots=at(6, 8)) == -3
+    assert call(f, a, pos=at(7, 4)) == -3
+    assert call(f, a, parents=at(11, 2)) == -3
 
 
 def test_qk_norm_rope_status(clib):
@@ -288,11 +303,15 @@ def test_qk_norm_rope_status(clib):
                    dict(wq=None), dict(eps=0.0), dict(eps=float("nan")), dict(eps=float("inf")),
                    dict(qkv=None), dict(table=None), dict(q=None), dict(v=None)):
         assert call(f, a, **change) == -1, change
-    for change in (dict(d=96), dict(rot=8), dict(rot=80), dict(N=1 << 30)):
+    for change in (dict(d=96), dict(rot=8), dict(rot=80), dict(N=1 << 30), dict(Hq=4093)):
         assert call(f, a, **change) == -2, change
+    # an output on the input, on another output, on the angles
+    for change in (dict(q=a["qkv"]), dict(v=at(6, 2 * 5 * 2 * 128 - 16)), dict(k=at(4, 16))):
+        assert call(f, a, **change) == -1, change
+    assert call(f, a, eps=1e-40) == -1
     for n in ("qkv", "wq", "wk", "table", "q", "k", "v"):
-        assert call(f, a, **{n: ctypes.c_void_p((20 << 12) + 8)}) == -3, n
-    assert call(f, a, pos=ctypes.c_void_p(4098)) == -3
+        assert call(f, a, **{n: at(20, 8)}) == -3, n
+    assert call(f, a, pos=at(30, 2)) == -3
     assert call(f, a, B=0) == 0 and call(f, a, N=0) == 0 and call(f, a, Hq=0, Hkv=0) == 0
 
 
@@ -304,9 +323,10 @@ def test_qk_norm_rope_paged_status(clib):
     for change in (dict(T=-1), dict(pages=-1), dict(ps=0), dict(pos=None), dict(slots=None),
                    dict(q=None), dict(k=None), dict(wk=None)):
         assert call(f, a, **change) == -1, change
+    assert call(f, a, v=a["k"]) == -1 and call(f, a, q=at(1, 256)) == -1
     assert call(f, a, d=32) == -2 and call(f, a, pages=1 << 20, ps=4096) == -2
-    assert call(f, a, slots=ctypes.c_void_p((9 << 12) + 4)) == -3
-    assert call(f, a, k=ctypes.c_void_p((6 << 12) + 8)) == -3
+    assert call(f, a, slots=at(9, 4)) == -3
+    assert call(f, a, k=at(6, 8)) == -3
     assert call(f, a, T=0) == 0
 
 
@@ -321,8 +341,9 @@ def test_qk_norm_rope_bwd_status(clib):
     need = clib.attn_qk_norm_rope_bwd_workspace_bytes(64)
     assert need == 592 * 2 * 64 * 4 and clib.attn_qk_norm_rope_bwd_workspace_bytes(0) == 0
     assert call(f, a, bytes=need - 1) == -6 and call(f, a, ws=None) == -6
-    assert call(f, a, dwq=ctypes.c_void_p(4098)) == -3
-    assert call(f, a, ws=ctypes.c_void_p((11 << 12) + 8)) == -3
+    assert call(f, a, dqkv=a["qkv"]) == -1 and call(f, a, ws=at(8)) == -1
+    assert call(f, a, dwq=at(30, 2)) == -3
+    assert call(f, a, ws=at(11, 8)) == -3
     assert call(f, a, wq=None, wk=None, B=0) == 0
 
 
@@ -340,9 +361,10 @@ def test_decode_tree_status(clib):
                    dict(P=1 << 20, ps=4096), dict(pages=1 << 30), dict(T=1 << 30)):
         assert call(f, a, **change) == -2, change
     for n in ("q", "k", "v", "o", "lse", "ws"):
-        assert call(f, a, **{n: ctypes.c_void_p((20 << 12) + 8)}) == -3, n
-    assert call(f, a, off=ctypes.c_void_p((6 << 12) + 2)) == -3
+        assert call(f, a, **{n: at(20, 8)}) == -3, n
+    assert call(f, a, off=at(6, 2)) == -3
     need = clib.attn_decode_tree_workspace_bytes(5, 4, 2, 4, 64, 0)
     assert need > 0 and clib.attn_decode_tree_workspace_bytes(0, 4, 2, 4, 64, 0) == 0
     assert call(f, a, bytes=need - 1) == -6 and call(f, a, ws=None) == -6
+    assert call(f, a, o=a["q"]) == -1 and call(f, a, lse=at(9, need - 16)) == -1
     assert call(f, a, T=0) == 0 and call(f, a, B=0) == 0 and call(f, a, nodes=0) == 0
