@@ -13,8 +13,8 @@
 // All of it is bound by the bytes: 2 to 3 passes over the rows and some ten operations a
 // value.  16 (d = 128) or 8 (d = 64) lanes hold a row, 16 bytes each, so loads and stores are
 // whole lines, the sums are shuffles, and a pair's other half is in the same lane
-// (interleaved) or a fixed number of lanes away.  A warp takes a chunk of a token's heads of
-// one kind (query, key or value): the angles and the gain are read and multiplied once,
+// (interleaved) or a fixed number of lanes away.  A warp takes a chunk of a token's query
+// heads or of its key and value heads: the angles and the gain are read and multiplied once,
 //   y = r (x A + x_partner B),  A = w cos,  B = +-w_partner sin,
 // and stay in registers for all rows of the chunk.  The rows come through shared memory, into
 // places that every lane fills and reads for itself (cp.async, no barrier): what is in flight
@@ -36,7 +36,7 @@ constexpr int kPrepThreads = 256;
 constexpr int kPrepWarps = kPrepThreads / 32;
 // Steps of a chunk at most, all in flight at once (a step is a row a lane: 2 or 4 rows a
 // warp).  Measured on a B200: [8, 4096] tokens of 32 + 2 x 32 heads of 128, forward: 8 steps
-// 241 us, 4 steps 267; [4, 4096] of 32 + 2 x 8, backward: 8 steps 101 us, 4 steps 111.
+// 240 us, 4 steps 267; [4, 4096] of 32 + 2 x 8, backward: 8 steps 101 us, 4 steps 111.
 constexpr int kChunkSteps = 8;
 // Blocks an SM: the forward at 64 registers a thread, the backward at 128 (with 80 it spills,
 // 128 us instead of 101).
@@ -188,28 +188,18 @@ __device__ __forceinline__ float inv_sqrt(float v) {
   return r;
 }
 
-// Chunks of a token: `steps` times the rows of a warp of one kind of head each.
+// Chunks of a token, `steps` times the rows of a warp each: of its query heads, and of its key
+// and value heads, which follow each other (with few of them one chunk has both: 281 -> 261 us
+// at 65536 tokens of 32 + 2 x 8 heads into a paged cache).
 struct Chunks {
-  int rows, q, kv;      // rows of a chunk; chunks of the query, and of the key or value heads
+  int rows, q, kv;
 
   __host__ __device__ Chunks(int Hq, int Hkv, int warp_rows, int steps)
-      : rows(warp_rows * steps), q((Hq + rows - 1) / rows), kv((Hkv + rows - 1) / rows) {}
-  __host__ __device__ int all() const { return q + 2 * kv; }
+      : rows(warp_rows * steps), q((Hq + rows - 1) / rows), kv((2 * Hkv + rows - 1) / rows) {}
+  __host__ __device__ int all() const { return q + kv; }
 };
 
 enum { kQuery = 0, kKey = 1, kValue = 2 };
-
-// Chunk c as its kind and its rows [h0, h1) among the heads of that kind.
-struct Span {
-  int kind, h0, h1, heads;
-
-  __device__ __forceinline__ Span(const Chunks& ch, int c, int Hq, int Hkv) {
-    kind = c < ch.q ? kQuery : c < ch.q + ch.kv ? kKey : kValue;
-    heads = kind == kQuery ? Hq : Hkv;
-    h0 = (kind == kQuery ? c : kind == kKey ? c - ch.q : c - ch.q - ch.kv) * ch.rows;
-    h1 = min(h0 + ch.rows, heads);
-  }
-};
 
 template <int D, bool kNorm, bool kInter, bool kPaged>
 __global__ void __launch_bounds__(kPrepThreads, kFwdBlocks)
@@ -222,59 +212,63 @@ attn_qk_prep_kernel(const PrepParams p, int steps) {
   const unsigned item = blockIdx.x * kPrepWarps + (threadIdx.x >> 5);
   const int t = (int)(item / (unsigned)ch.all());
   if (t >= p.tokens) return;
-  const Span sp(ch, (int)(item - (unsigned)t * ch.all()), p.Hq, p.Hkv);
-  const int kind = sp.kind;
+  const int c = (int)(item - (unsigned)t * ch.all());
+  const bool is_q = c < ch.q;
+  // rows [h0, h1) of the query heads, or of the key heads and the value heads behind them
+  const int h0 = (is_q ? c : c - ch.q) * ch.rows;
+  const int h1 = min(h0 + ch.rows, is_q ? p.Hq : 2 * p.Hkv);
   const uint32_t mine = smem_u32(&rows[0][threadIdx.x]);
   constexpr uint32_t kSlot = kPrepThreads * 16;
   // the first of two loads, one after the other, on the way to the angles
   const int pos = kPaged || p.positions != nullptr ? __ldg(p.positions + t) : t % p.N;
 
   {
-    const int head0 = kind == kQuery ? 0 : kind == kKey ? p.Hq : p.Hq + p.Hkv;
     const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.qkv) +
-                               ((size_t)t * p.H + head0) * D + e0;
+                               ((size_t)t * p.H + (is_q ? 0 : p.Hq)) * D + e0;
 #pragma unroll
     for (int i = 0; i < kChunkSteps; ++i) {
-      const int h = sp.h0 + i * R::kRows + sub;
-      if (i < steps) copy16(mine + i * kSlot, src + min(h, sp.h1 - 1) * D, h < sp.h1);
+      const int h = h0 + i * R::kRows + sub;
+      if (i < steps) copy16(mine + i * kSlot, src + min(h, h1 - 1) * D, h < h1);
       if (i == kChunkSteps / 2 - 1 || i == kChunkSteps - 1) copy_commit();
     }
   }
 
-  // this lane's part of the token's row of head h0 + sub, and what the next step adds
-  size_t dst, dst_step;
+  // this lane's part of the token's row of head 0 (of the query, or the key and value heads),
+  // and what a head adds
+  size_t dst, head;
   bool keep = true;
   if (kPaged) {
-    if (kind == kQuery) {
+    if (is_q) {
       dst = (size_t)t * p.Hq * D;
-      dst_step = D;
+      head = D;
     } else {
       const long long s = __ldg(p.slots + t);
       keep = s >= 0 && s < p.num_slots;
       const int place = keep ? (int)s : 0;
       const int page = place / p.page_size;
       dst = ((size_t)page * p.Hkv * p.page_size + (size_t)(place - page * p.page_size)) * D;
-      dst_step = (size_t)p.page_size * D;
+      head = (size_t)p.page_size * D;
     }
   } else {
     const int b = t / p.N, n = t - b * p.N;
-    dst = ((size_t)b * sp.heads * p.N + n) * D;
-    dst_step = (size_t)p.N * D;
+    dst = ((size_t)b * (is_q ? p.Hq : p.Hkv) * p.N + n) * D;
+    head = (size_t)p.N * D;
   }
-  __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(kind == kQuery ? p.q
-                                                        : kind == kKey ? p.k : p.v) +
-                       dst + (sp.h0 + sub) * dst_step + e0;
-  dst_step *= R::kRows;
-  // rows of this lane in the chunk (0: the token has no place)
-  const int n_rows = keep && sp.h0 + sub < sp.h1 ? (sp.h1 - sp.h0 - sub - 1) / R::kRows + 1 : 0;
-  const int n_steps = (sp.h1 - sp.h0 - 1) / R::kRows + 1;
+  dst += e0;
+  __nv_bfloat16* const v_out = reinterpret_cast<__nv_bfloat16*>(p.v) + dst;
+  const int first_v = is_q ? h1 : p.Hkv;      // rows from here on are values
+  int h = h0 + sub;
+  __nv_bfloat16* out = h < first_v || is_q
+                           ? reinterpret_cast<__nv_bfloat16*>(is_q ? p.q : p.k) + dst + h * head
+                           : v_out + (h - first_v) * head;
+  const int n_steps = (h1 - h0 - 1) / R::kRows + 1;
 
   Angles<kInter> ang;
-  if (kind != kValue) {
+  if (h0 < first_v) {
     ang.place(p, e0, lane);
     ang.template load<false>(p, pos, e0);
     if (kNorm) {      // A = w c, B = w_partner s
-      const uint4 w = load_gain(kind == kQuery ? p.wq : p.wk, e0);
+      const uint4 w = load_gain(is_q ? p.wq : p.wk, e0);
       float g[8];
       unpack8(w, g);
 #pragma unroll
@@ -291,7 +285,7 @@ attn_qk_prep_kernel(const PrepParams p, int steps) {
 #pragma unroll 1
     for (int i = half * (kChunkSteps / 2); i < end; ++i) {
       uint4 x = read16(mine + i * kSlot);
-      if (kind != kValue) {
+      if (h - sub < first_v) {      // not all of the warp's rows are values
         float v[8], vp[8];
         unpack8(x, v);
         ang.partners(x, vp);
@@ -308,10 +302,12 @@ attn_qk_prep_kernel(const PrepParams p, int steps) {
           ffma2(v[j], v[j + 1], vp[j], vp[j + 1], ang.s[j], ang.s[j + 1], v[j], v[j + 1]);
           if (kNorm) fmul2(v[j], v[j + 1], v[j], v[j + 1], r, r);
         }
-        x = pack8(v);
+        if (h < first_v) x = pack8(v);
       }
-      if (i < n_rows) store8(out, 0, x);
-      out += dst_step;
+      if (h < h1 && keep) store8(out, 0, x);
+      out += R::kRows * head;
+      h += R::kRows;
+      if (h >= first_v && h - R::kRows < first_v) out = v_out + (h - first_v) * head;
     }
   }
 }
