@@ -203,7 +203,7 @@ enum { kQuery = 0, kKey = 1, kValue = 2 };
 
 template <int D, bool kNorm, bool kInter, bool kPaged>
 __global__ void __launch_bounds__(kPrepThreads, kFwdBlocks)
-attn_qk_prep_kernel(const PrepParams p, int steps) {
+attn_qk_prep_kernel(const PrepParams p, int steps, int ahead) {
   using R = Row<D>;
   __shared__ __align__(16) uint4 rows[kChunkSteps][kPrepThreads];
   const int lane = threadIdx.x & 31;
@@ -221,6 +221,10 @@ attn_qk_prep_kernel(const PrepParams p, int steps) {
   constexpr uint32_t kSlot = kPrepThreads * 16;
   // the first of two loads, one after the other, on the way to the angles
   const int pos = kPaged || p.positions != nullptr ? __ldg(p.positions + t) : t % p.N;
+  // the position of a token that warps launched a wave later will take
+  int later = -1;
+  if (c == 0 && (kPaged || p.positions != nullptr) && t + ahead < p.tokens)
+    later = __ldg(p.positions + t + ahead);
 
   {
     const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.qkv) +
@@ -310,6 +314,10 @@ attn_qk_prep_kernel(const PrepParams p, int steps) {
       if (h >= first_v && h - R::kRows < first_v) out = v_out + (h - first_v) * head;
     }
   }
+  // its angles on their way to L2 meanwhile: rows of a large table come from memory, and a
+  // warp's start would wait for the position and then for them
+  if ((unsigned)later < (unsigned)p.table_rows && lane * 32 < p.rot)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.table + (size_t)later * p.rot + lane * 32));
 }
 
 // Backward.  A block takes a run of tokens and goes through their query chunks, then their key
@@ -353,7 +361,7 @@ attn_qk_prep_bwd_kernel(const PrepBwdParams pb, int steps) {
 
     // An item's token, and this lane's first row of it: offsets in the input and the gradient,
     // and how many of its steps have a row for this lane.
-    int t, n_rows;
+    int t, n_rows, pos;
     size_t in, dy_in;
     auto aim = [&](int item) {
       t = item / chunks;
@@ -363,6 +371,8 @@ attn_qk_prep_bwd_kernel(const PrepBwdParams pb, int steps) {
       in = ((size_t)t * p.H + head0 + h) * D + e0;
       dy_in = (((size_t)b * heads + h) * p.N + (t - b * p.N)) * D + e0;
       n_rows = h < heads ? min((heads - h - 1) / R::kRows + 1, n_steps) : 0;
+      // (read an item ahead: the angles wait for it)
+      pos = p.positions != nullptr ? __ldg(p.positions + t) : t - b * p.N;
     };
     const __nv_bfloat16 *cx = nullptr, *cdy = nullptr;
     const __nv_bfloat16* any = reinterpret_cast<const __nv_bfloat16*>(p.qkv);   // for no row
@@ -388,8 +398,7 @@ attn_qk_prep_bwd_kernel(const PrepBwdParams pb, int steps) {
       }
     }
     for (; item < items; item += kPrepWarps) {
-      if (kind != kValue)
-        ang.template load<true>(p, p.positions != nullptr ? __ldg(p.positions + t) : t % p.N, e0);
+      if (kind != kValue) ang.template load<true>(p, pos, e0);
       __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(pb.dqkv) + in;
       const int rows = n_rows;
       const bool more = item + kPrepWarps < items;
@@ -502,10 +511,14 @@ int launch_fwd_t(const PrepParams& p, bool paged, int num_sms, cudaStream_t stre
   const int steps = chunk_steps(p.tokens, p.Hq, p.Hkv, Row<D>::kRows, num_sms);
   const long long items = (long long)p.tokens * Chunks(p.Hq, p.Hkv, Row<D>::kRows, steps).all();
   const unsigned blocks = (unsigned)((items + kPrepWarps - 1) / kPrepWarps);   // items < 2^31
+  const int ahead = kFwdBlocks * num_sms * kPrepWarps /
+                    Chunks(p.Hq, p.Hkv, Row<D>::kRows, steps).all();
   if (paged)
-    attn_qk_prep_kernel<D, kNorm, kInter, true><<<blocks, kPrepThreads, 0, stream>>>(p, steps);
+    attn_qk_prep_kernel<D, kNorm, kInter, true>
+        <<<blocks, kPrepThreads, 0, stream>>>(p, steps, ahead);
   else
-    attn_qk_prep_kernel<D, kNorm, kInter, false><<<blocks, kPrepThreads, 0, stream>>>(p, steps);
+    attn_qk_prep_kernel<D, kNorm, kInter, false>
+        <<<blocks, kPrepThreads, 0, stream>>>(p, steps, ahead);
   return cudaGetLastError() == cudaSuccess ? 0 : -4;
 }
 
