@@ -480,6 +480,13 @@ def attn_page_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages:
     the tokens of drafted trees positions by depth; ``free_used`` is the pages_used of an
     earlier step on the same free list; ``held_rows`` (int32 [B]) are the rows that already
     have pages, where rejected drafts made them more than ctx_lens."""
+    if stream is not None:
+        with torch.cuda.stream(stream):     # what the call allocates is that stream's too
+            return attn_page_tables(
+                ctx_lens, new_lens, free_pages, block_table, page_size=page_size,
+                num_tokens=num_tokens, free_used=free_used, held_rows=held_rows, parents=parents,
+                slots=slots, positions=positions, seq_lens=seq_lens,
+                token_offsets=token_offsets, pages_used=pages_used)
     lib = _lib.load()
     i32 = torch.int32
     _need(ctx_lens, "ctx_lens", i32, 1)
@@ -512,7 +519,7 @@ def attn_page_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages:
                                   _ptr(free_used), _ptr(held_rows), _ptr(parents),
                                   _ptr(block_table), _ptr(slots), _ptr(positions),
                                   _ptr(seq_lens), _ptr(token_offsets), _ptr(pages_used), B, max_pages, int(page_size),
-                                  num_free, T, _stream(ctx_lens.device, stream))
+                                  num_free, T, _stream(ctx_lens.device))
     _check(st, "attn_page_tables")
     return slots, positions, seq_lens, token_offsets, pages_used
 
@@ -546,6 +553,11 @@ def attn_qk_norm_rope(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
 
     Gains bf16 [d] (both None: no norm); rope_table fp32 [rows, rot], cos | sin of each
     position's rot/2 angles (None: no rotation); positions int32 [B,N] (None: 0..N-1)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):     # what the call allocates is that stream's too
+            return attn_qk_norm_rope(qkv, q_weight, k_weight, rope_table,
+                                     num_q_heads=num_q_heads, positions=positions, eps=eps,
+                                     interleaved=interleaved, q=q, k=k, v=v)
     lib = _lib.load()
     rot, rows = _prep_inputs(qkv, 4, q_weight, k_weight, rope_table)
     B, N, H, d = qkv.shape
@@ -561,7 +573,7 @@ def attn_qk_norm_rope(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
         st = lib.attn_qk_norm_rope(_ptr(qkv), _ptr(q_weight), _ptr(k_weight), _ptr(rope_table),
                                    _ptr(positions), _ptr(q), _ptr(k), _ptr(v), B, N, Hq, Hkv, d,
                                    rot, rows, float(eps), int(bool(interleaved)),
-                                   _stream(qkv.device, stream))
+                                   _stream(qkv.device))
     _check(st, "attn_qk_norm_rope")
     return q, k, v
 
@@ -576,6 +588,12 @@ def attn_qk_norm_rope_bwd(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
                           workspace: Optional[torch.Tensor] = None, stream=None):
     """Backward of attn_qk_norm_rope: (dqkv bf16 as qkv, dq_weight fp32 [d], dk_weight fp32 [d])
     from qkv and attn_bwd's (dq, dk, dv); the gains' gradients are None without a norm."""
+    if stream is not None:
+        with torch.cuda.stream(stream):     # what the call allocates is that stream's too
+            return attn_qk_norm_rope_bwd(
+                qkv, q_weight, k_weight, rope_table, dq, dk, dv, positions=positions, eps=eps,
+                interleaved=interleaved, dqkv=dqkv, dq_weight=dq_weight, dk_weight=dk_weight,
+                workspace=workspace)
     lib = _lib.load()
     rot, rows = _prep_inputs(qkv, 4, q_weight, k_weight, rope_table)
     B, N, H, d = qkv.shape
@@ -607,7 +625,7 @@ def attn_qk_norm_rope_bwd(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
                                        _ptr(dv), _ptr(dqkv), _ptr(dq_weight), _ptr(dk_weight), B,
                                        N, Hq, Hkv, d, rot, rows, float(eps),
                                        int(bool(interleaved)), _ptr(workspace), ws_bytes,
-                                       _stream(qkv.device, stream))
+                                       _stream(qkv.device))
     _check(st, "attn_qk_norm_rope_bwd")
     return dqkv, dq_weight, dk_weight
 
@@ -625,6 +643,11 @@ def attn_qk_norm_rope_paged(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
     """attn_qk_norm_rope for packed tokens qkv bf16 [T,Hq+2*Hkv,d]: returns q [T,Hq,d] and
     writes the K and V rows of each token into pages [num_pages,Hkv,page_size,d] at its slot
     (int64 [T]; a slot outside the cache writes nothing).  positions int32 [T]."""
+    if stream is not None:
+        with torch.cuda.stream(stream):     # what the call allocates is that stream's too
+            return attn_qk_norm_rope_paged(
+                qkv, q_weight, k_weight, rope_table, positions, slots, k_pages, v_pages, eps=eps,
+                interleaved=interleaved, q=q)
     lib = _lib.load()
     rot, rows = _prep_inputs(qkv, 3, q_weight, k_weight, rope_table)
     T, H, d = qkv.shape
@@ -644,7 +667,7 @@ def attn_qk_norm_rope_paged(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
                                          _ptr(rope_table), _ptr(positions), _ptr(slots), _ptr(q),
                                          _ptr(k_pages), _ptr(v_pages), T, Hq, Hkv, d, num_pages,
                                          page_size, rot, rows, float(eps),
-                                         int(bool(interleaved)), _stream(qkv.device, stream))
+                                         int(bool(interleaved)), _stream(qkv.device))
     _check(st, "attn_qk_norm_rope_paged")
     return q
 
@@ -667,6 +690,11 @@ def attn_decode_tree(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
 
     parents int32 [T]: index within the sequence of the node each token hangs on, -1 for the
     context; None: a chain.  Rows behind token_offsets[B] are left as they were."""
+    if stream is not None:
+        with torch.cuda.stream(stream):     # what the call allocates is that stream's too
+            return attn_decode_tree(
+                q, k_pages, v_pages, block_table, seq_lens, token_offsets, max_nodes=max_nodes,
+                parents=parents, scale=scale, workspace=workspace, out=out, lse=lse)
     lib = _lib.load()
     bf16, i32 = torch.bfloat16, torch.int32
     _need(q, "q", bf16, 3)
@@ -693,7 +721,7 @@ def attn_decode_tree(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
                                   _ptr(seq_lens), _ptr(token_offsets), _ptr(parents), _ptr(out),
                                   _ptr(lse), B, T, Hq, Hkv, num_pages, page_size, max_pages,
                                   int(max_nodes), d, float(scale or 0.0), _ptr(workspace),
-                                  ws_bytes, _stream(q.device, stream))
+                                  ws_bytes, _stream(q.device))
     _check(st, "attn_decode_tree")
     return out, lse
 

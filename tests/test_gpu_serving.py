@@ -467,6 +467,82 @@ def test_tree_garbage_past_the_end_of_long_sequences():
     assert np.abs(f64(lse) - L).max() <= 1e-4
 
 
+def test_tree_values_that_are_no_numbers_stay_with_the_rows_that_see_them():
+    lens, n = [700, 2000], [6, 5]
+    q, kp, vp, table, offsets, _ = tree_inputs(lens, n, 4, 2, 64, 64, 18)
+    par = np.array([-1, 0, 0, 1, 2, -1, -1, 0, 0, 1, 2])
+    q[7, 1] = float("nan")                      # a query row: sequence 1, node 1, head 1
+    q[9, 2, 5] = float("inf")
+    k_row = 700 - 6 + 2                         # the key of sequence 0's node 2, KV head 0
+    kp[int(table[0, k_row // 64]), 0, k_row % 64, 3] = float("nan")
+    bad = np.zeros((11, 4), bool)
+    bad[7, 1] = bad[9, 2] = True
+    bad[[2, 4], :2] = True                      # node 2 and its descendant see that key
+    out, lse = attn_decode_tree(q, kp, vp, i32(table), i32(lens), i32(offsets), max_nodes=6,
+                                parents=i32(par))
+    assert device_status() == 0
+    assert np.array_equal(np.isnan(f64(lse)), bad)
+    assert np.isnan(f64(out)[bad]).all()
+    q, kp = torch.nan_to_num(q, posinf=1.0), torch.nan_to_num(kp)
+    O, L, A = oracle.decode_tree(f64(q), f64(kp), f64(vp), table, lens, offsets, par)
+    within(f64(out)[~bad], O[~bad], 1.02 * BF * (np.abs(O) + A)[~bad], "O")
+    assert np.abs(f64(lse) - L)[~bad].max() <= 1e-4
+
+
+def test_tree_cache_past_32_bit_offsets():
+    # 2.6 G values a cache: the sequences' pages lie at its end and its beginning
+    pages, Hkv, page, d = 40000, 8, 64, 128
+    kp, vp = (torch.empty((pages, Hkv, page, d), dtype=torch.bfloat16, device="cuda")
+              for _ in range(2))
+    table = np.array([[pages - 1, 0, pages - 3], [1, pages - 2, 20000]])
+    small = [randn((6, Hkv, page, d), 91, i) for i in range(2)]
+    for big, few in zip((kp, vp), small):
+        big[torch.from_numpy(table.reshape(-1)).cuda()] = few
+    q = randn((9, 16, d), 92)
+    lens, offsets = [170, 130], [0, 5, 9]
+    out, lse = attn_decode_tree(q, kp, vp, i32(table), i32(lens), i32(offsets), max_nodes=5)
+    assert device_status() == 0
+    O, L, A = oracle.decode_tree(f64(q), f64(small[0]), f64(small[1]), np.arange(6).reshape(2, 3),
+                                 lens, offsets)
+    within(out, O, 1.02 * BF * (np.abs(O) + A), "O")
+    assert np.abs(f64(lse) - L).max() <= 1e-4
+    # and written there: slots of the last page and of the first
+    x, w, rp = prep_inputs(4, 16, Hkv, d, 128, True, 93)
+    slots = np.array([(pages - 1) * page + 63, 0, pages * page - 64, 5])
+    q = attn_qk_norm_rope_paged(x, *w, rp, i32([7, 8, 9, 10]), torch.from_numpy(slots).cuda(), kp,
+                                vp, eps=1e-5)
+    want, bound = prep_expected(x, w, rp, [7, 8, 9, 10], 16, 1e-5, False)
+    within(q, want[0], bound[0], "q")
+    for cache, o, e in ((kp, want[1], bound[1]), (vp, want[2], bound[2])):
+        sl = torch.from_numpy(slots).cuda()
+        within(cache[sl // page, :, sl % page], o, e, "cache")
+
+
+def test_qk_norm_rope_past_32_bit_offsets():
+    # 2.3 G values in and out; tokens of both ends are checked, forward and backward
+    B, N, Hq, Hkv, d = 3, 61440 + 3, 64, 16, 128
+    x = torch.randn((B, N, Hq + 2 * Hkv, d), device="cuda", dtype=torch.bfloat16)
+    assert x.numel() > 2 ** 31
+    w = tuple((1 + 0.3 * randn((d,), 95, k).float()).bfloat16() for k in (1, 2))
+    table = rope(N, 64)
+    q, k, v = attn_qk_norm_rope(x, *w, table, num_q_heads=Hq, eps=1e-5)
+    at = np.array([0, 1, N - 2, N - 1])
+    for b in (0, B - 1):
+        few = x[b, at].contiguous()
+        want, bound = prep_expected(few, w, table, at, Hq, 1e-5, False)
+        for got, o, e, name in zip((q, k, v), want, bound, "qkv"):
+            within(got[b][:, at].transpose(0, 1), o, e, name)
+    dx, _, _ = attn_qk_norm_rope_bwd(x, *w, table, q, k, v, eps=1e-5)
+    for b in (0, B - 1):
+        few = f64(x[b, at])
+        g = [f64(t[b][:, at].transpose(0, 1)) for t in (q, k, v)]
+        want, _, _ = oracle.qk_norm_rope_backward(few, f64(w[0]), f64(w[1]), f64(table), at, *g,
+                                                  1e-5)
+        # dy = y here, so t and x M nearly cancel: fp32 leaves 40 u of the terms, which are
+        # below 16 (gains below 2, |y| below 8)
+        within(dx[b, at], want, BF * np.abs(want) + 40 * U * 32, "dqkv")
+
+
 def test_tree_pages_outside_the_cache_read_zeros():
     q, kp, vp, table, offsets, par = tree_inputs([200, 100], [3, 4], 4, 2, 64, 64, 15)
     table[0, 1], table[1, 0] = -1, kp.shape[0]
@@ -649,6 +725,33 @@ def test_a_wait_that_runs_out_is_reported_and_later_calls_run(nodes):
     again = attn_decode_tree(*args, max_nodes=nodes, parents=i32(par))
     assert device_status() == 0
     assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
+def test_calls_on_a_given_stream():
+    # the whole call, its allocations too, belongs to the stream that is given
+    s = _step_state(85)
+    fresh = {n: t.clone() for n, t in s.items()}
+    want = _step_outputs()
+    _step(fresh, want)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    slots, pos, lens, off, used = attn_page_tables(
+        s["ctx"], s["new"], s["free"], s["table"], page_size=64, num_tokens=48,
+        free_used=s["used"], parents=s["parents"], stream=st)
+    q = attn_qk_norm_rope_paged(s["qkv"], s["wq"], s["wk"], s["rope"], pos, slots, s["k"], s["v"],
+                                stream=st)
+    o, lse = attn_decode_tree(q, s["k"], s["v"], s["table"], lens, off, max_nodes=9,
+                              parents=s["parents"], stream=st)
+    x = s["qkv"].view(1, 48, 8, 64)
+    qq, kk, vv = attn_qk_norm_rope(x, s["wq"], s["wk"], s["rope"], num_q_heads=4, stream=st)
+    dx, dwq, dwk = attn_qk_norm_rope_bwd(x, s["wq"], s["wk"], s["rope"], qq, kk, vv, stream=st)
+    st.synchronize()
+    assert device_status() == 0
+    n = int(off[-1])
+    assert torch.equal(q, want["q"]) and torch.equal(o[:n], want["out"][:n])
+    assert torch.equal(slots, want["slots"]) and torch.equal(s["k"], fresh["k"])
+    again = attn_qk_norm_rope_bwd(x, s["wq"], s["wk"], s["rope"], qq, kk, vv)
+    assert torch.equal(dx, again[0]) and torch.equal(dwq, again[1]) and torch.equal(dwk, again[2])
 
 
 def test_empty_calls():

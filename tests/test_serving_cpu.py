@@ -47,7 +47,8 @@ def test_page_tables_keeps_the_pages_of_rejected_rows():
     assert slots.tolist() == [27, 28, 29, 30, 31]
     # more than the table has, or less than the rows
     assert oracle.page_tables([3], [5], [9], table, held_rows=[99], **args)[4].tolist() == [0]
-    assert oracle.page_tables([3], [5], [9], table, held_rows=[-1], **args)[5].tolist() == [[6, 9, 0]]
+    none = oracle.page_tables([3], [5], [9], table, held_rows=[-1], **args)
+    assert none[5].tolist() == [[6, 9, 0]]
 
 
 def test_tree_depth_and_bad_parents():
@@ -95,13 +96,16 @@ def test_gradients_against_differences(interleaved, with_norm):
         step = np.zeros(x.size)
         step[i] = h
         step = step.reshape(x.shape)
-        assert abs((loss(x + step, *w) - loss(x - step, *w)) / (2 * h) - dx.reshape(-1)[i]) < 1e-6
+        diff = (loss(x + step, *w) - loss(x - step, *w)) / (2 * h)
+        assert abs(diff - dx.reshape(-1)[i]) < 1e-6
     if with_norm:
         for i in (0, 17, 63):
             e = np.zeros(d)
             e[i] = h
-            assert abs((loss(x, w[0] + e, w[1]) - loss(x, w[0] - e, w[1])) / (2 * h) - dwq[i]) < 1e-6
-            assert abs((loss(x, w[0], w[1] + e) - loss(x, w[0], w[1] - e)) / (2 * h) - dwk[i]) < 1e-6
+            diff = (loss(x, w[0] + e, w[1]) - loss(x, w[0] - e, w[1])) / (2 * h)
+            assert abs(diff - dwq[i]) < 1e-6
+            diff = (loss(x, w[0], w[1] + e) - loss(x, w[0], w[1] - e)) / (2 * h)
+            assert abs(diff - dwk[i]) < 1e-6
 
 
 def test_tree_is_attention_on_the_rows_of_each_path():
@@ -120,7 +124,8 @@ def test_tree_is_attention_on_the_rows_of_each_path():
         n, L = (4, 100) if b == 0 else (2, 130)
         K, V = (oracle.gather_paged(p, table[b], L) for p in (kp, vp))
         rows = list(range(L - n)) + [L - n + j for j in path]
-        want, want_l = oracle.attention(q[t][None, :, None], K[None][:, :, rows], V[None][:, :, rows])
+        want, want_l = oracle.attention(q[t][None, :, None], K[None][:, :, rows],
+                                        V[None][:, :, rows])
         assert np.allclose(O[t], want[0, :, 0], atol=1e-12)
         assert np.allclose(lse[t], want_l[0, :, 0], atol=1e-12)
 
@@ -278,8 +283,9 @@ def call(fn, args, **change):
 
 
 def test_page_tables_status(clib):
-    a = dict(ctx=at(1), new=at(2), free=at(3), used=at(4), held=at(12), parents=None, table=at(5), slots=at(6),
-             pos=at(7), lens=at(8), off=at(9), out=at(10), B=3, P=7, ps=64, nf=9, T=11, stream=None)
+    a = dict(ctx=at(1), new=at(2), free=at(3), used=at(4), held=at(12), parents=None,
+             table=at(5), slots=at(6), pos=at(7), lens=at(8), off=at(9), out=at(10), B=3, P=7,
+             ps=64, nf=9, T=11, stream=None)
     f = clib.attn_page_tables
     for change in (dict(B=-1), dict(P=-1), dict(ps=0), dict(nf=-1), dict(T=-1), dict(ctx=None),
                    dict(new=None), dict(free=None), dict(table=None), dict(slots=None),
