@@ -69,7 +69,11 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                     pack_bf16x2(x[6], x[7]));
 }
 
-// 16 bytes to this lane's place in shared memory, or zeros.
+// 16 bytes to this lane's place in shared memory.
+__device__ __forceinline__ void copy16(uint32_t dst, const __nv_bfloat16* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// The same, or zeros.
 __device__ __forceinline__ void copy16(uint32_t dst, const __nv_bfloat16* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(valid ? 16 : 0)
@@ -231,12 +235,22 @@ attn_qk_prep_kernel(const PrepParams p, int steps, int ahead) {
   {
     const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(p.qkv) +
                                ((size_t)t * p.H + (is_q ? 0 : p.Hq)) * D + e0;
+    if (h1 - h0 == kChunkSteps * R::kRows) {      // a full chunk, as most are
+      const __nv_bfloat16* from = src + (h0 + sub) * D;
 #pragma unroll
-    for (int i = 0; i < kChunkSteps; ++i) {
-      const int h = h0 + i * R::kRows + sub;
-      if (i < steps) copy16(mine + i * kSlot, src + min(h, h1 - 1) * D, h < h1);
-      if (i == kChunkSteps / 2 - 1 || i == kChunkSteps - 1) copy_commit();
+      for (int i = 0; i < kChunkSteps; ++i) {
+        copy16(mine + i * kSlot, from + i * R::kRows * D);
+        if (i == kChunkSteps / 2 - 1) copy_commit();
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kChunkSteps; ++i) {
+        const int h = h0 + i * R::kRows + sub;
+        if (i < steps) copy16(mine + i * kSlot, src + min(h, h1 - 1) * D, h < h1);
+        if (i == kChunkSteps / 2 - 1) copy_commit();
+      }
     }
+    copy_commit();
   }
 
   // this lane's part of the token's row of head 0 (of the query, or the key and value heads),
