@@ -415,9 +415,8 @@ ATTN_API int attn_qk_norm_rope_paged(const void* qkv, const void* q_weight, cons
  *            attn_decode_tree_workspace_bytes bytes
  * Rows of q behind token_offsets[B], and between a sequence's max_nodes and its end, are
  * left as they were in o and lse.  A node that sees no row (seq_lens below n) gets O = 0 and
- * LSE = -inf.  What a page holds past the sequence's end is not used, whatever it is; rows
- * inside the length take part in one product for all nodes of the sequence, so a NaN or
- * infinity in V there may reach nodes that do not see its row.
+ * LSE = -inf.  What a page holds past the sequence's end is not used, whatever it is, and an
+ * infinity or NaN in a drafted row reaches only the nodes that see the row.
  * Hq / Hkv <= 16, d in {64, 128}, page_size a multiple of 64.  o, lse and the workspace may not
  * overlap an input or each other (INVALID_ARG).
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, CUDA.

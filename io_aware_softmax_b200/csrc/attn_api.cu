@@ -936,6 +936,7 @@ extern "C" int attn_decode_tree(const void* q, const void* k_pages, const void* 
   if (scale <= 0.f) scale = 1.0f / std::sqrt((float)d);
 
   TreeParams p{};
+  p.v_pages = v_pages;
   p.block_table = block_table;
   p.seq_lens = seq_lens;
   p.offsets = token_offsets;

@@ -86,6 +86,7 @@ struct TreeParams {
   const int* seq_lens;      // [B]
   const int* offsets;       // [B + 1]
   const int* parents;       // [T] or null (a chain)
+  const void* v_pages;      // bf16 [num_pages, Hkv, page_size, d]: for values that are no numbers
   void* o;                  // bf16 [T, Hq, d]
   float* lse;               // fp32 [T, Hq]
   // workspace: prefix sums of the sequences' units, then the pieces' partial results

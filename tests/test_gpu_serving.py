@@ -489,6 +489,37 @@ def test_tree_values_that_are_no_numbers_stay_with_the_rows_that_see_them():
     assert np.abs(f64(lse) - L)[~bad].max() <= 1e-4
 
 
+@pytest.mark.parametrize("d,Hq,nodes", [(64, 4, 7), (128, 4, 7), (64, 16, 40), (128, 16, 40),
+                                        (128, 2, 120)])
+def test_tree_values_that_are_no_numbers_in_hidden_rows(d, Hq, nodes):
+    # infinities and NaN in K and V of drafted rows reach the nodes that see them and no other:
+    # whole and cut sequences, rows of one tile and of two, few query rows and many
+    lens = [nodes, 100 + nodes, 128 + nodes // 2, 3000 + nodes, 77]
+    n = [nodes, nodes, nodes // 2, nodes, 3]
+    q, kp, vp, table, offsets, par = tree_inputs(lens, n, Hq, 2, d, 64, d + nodes, branch=3)
+    rng = np.random.default_rng(nodes)
+    for b, (length, m) in enumerate(zip(lens[:4], n)):
+        for cache, value in ((vp, "nan"), (vp, "inf"), (vp, "-inf"), (kp, "nan")):
+            for _ in range(2):
+                row = length - m + int(rng.integers(m // 2, m))
+                cache[int(table[b, row // 64]), int(rng.integers(2)), row % 64,
+                      int(rng.integers(d))] = float(value)
+    with np.errstate(invalid="ignore"):
+        O, L, A = oracle.decode_tree(f64(q), f64(kp), f64(vp), table, lens, offsets, par)
+    assert np.isnan(O).any() and np.isinf(O).any() and np.isfinite(O).mean() > 0.3
+    out, lse = attn_decode_tree(q, kp, vp, i32(table), i32(lens), i32(offsets), max_nodes=nodes,
+                                parents=i32(par))
+    assert device_status() == 0
+    got, fin = f64(out), np.isfinite(O)
+    assert np.array_equal(np.isnan(got), np.isnan(O)) and np.array_equal(got[np.isinf(O)],
+                                                                         O[np.isinf(O)])
+    # A is not finite beside an infinity of the same row's sum: |V| up to 6 bounds it there
+    bound = 1.02 * BF * (np.abs(O) + np.where(np.isfinite(A), A, 6.0))
+    within(got[fin], O[fin], bound[fin], "O")
+    ok = np.isfinite(L)
+    assert np.array_equal(np.isfinite(f64(lse)), ok) and np.abs(f64(lse) - L)[ok].max() <= 1e-4
+
+
 def test_tree_cache_past_32_bit_offsets():
     # 2.6 G values a cache: the sequences' pages lie at its end and its beginning
     pages, Hkv, page, d = 40000, 8, 64, 128
