@@ -34,6 +34,11 @@ struct Sums {
   long long tokens, pages;
 };
 
+// A block's shared memory beside the 12 bytes a sequence.
+struct BlockShared {
+  Sums warp_sums[2][kPagesWarps];
+};
+
 __device__ __forceinline__ Sums block_scan(Sums v, Sums* warp_sums, Sums& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   Sums x = v;
@@ -68,7 +73,7 @@ __global__ void __launch_bounds__(kPagesThreads) attn_page_tables_kernel(const P
   int* off = smem;                  // [B + 1] first token of each sequence
   int* held = smem + p.B + 1;       // [B] cache rows before the step
   int* first = held + p.B;          // [B] free-list index of the first new page
-  __shared__ Sums warp_sums[2][kPagesWarps];
+  __shared__ BlockShared sh;
   const int tid = threadIdx.x;
   const int cap = p.max_pages * p.page_size;        // below 2^31 (host check)
   const int per = (p.B + kPagesThreads - 1) / kPagesThreads;
@@ -94,7 +99,7 @@ __global__ void __launch_bounds__(kPagesThreads) attn_page_tables_kernel(const P
     mine.pages += max(pages_of(grown(c, n)) - owned(b, c), 0);
   }
   const long long used0 = p.free_used != nullptr ? max(__ldg(p.free_used), 0) : 0;
-  Sums run = block_scan(mine, warp_sums[0], total);
+  Sums run = block_scan(mine, sh.warp_sums[0], total);
   if (total.tokens > p.num_tokens) {
     // more tokens than there is room for: the lengths that count are cut, and the pages follow
     long long t = run.tokens;
@@ -106,7 +111,7 @@ __global__ void __launch_bounds__(kPagesThreads) attn_page_tables_kernel(const P
       mine.pages += max(pages_of(e) - owned(b, held[b]), 0);
       t += n;
     }
-    run = block_scan(mine, warp_sums[1], total);
+    run = block_scan(mine, sh.warp_sums[1], total);
   }
   run.pages += used0;
   total.pages += used0;
@@ -232,7 +237,8 @@ int launch_page_tables(const PagesParams& args, int num_sms, cudaStream_t stream
   page_divisor(p.page_size, p.div_mul, p.div_shift);
   const int smem = (3 * p.B + 1) * 4;
   static std::atomic<bool> ready[64];
-  if (smem > 48 * 1024 &&
+  // without the attribute a block has 48 KB, of which the fixed part comes first
+  if (smem + (int)sizeof(BlockShared) > 48 * 1024 &&
       !allow_smem(reinterpret_cast<const void*>(attn_page_tables_kernel),
                   (3 * kPagesMaxSeqs + 1) * 4, ready))
     return -4;

@@ -12,6 +12,10 @@ Tolerances count roundings.  bf16 rounds by at most 2^-8 of the value, fp32 by 2
   steps.  LSE: a score is off by at most (d + 2) u of scale sum_c |q_c k_c|, and the sum of
   exponentials, its joins, the base-2 logarithm and the exponential by 600 u.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -89,6 +93,24 @@ def test_page_tables_edges():
     check_tables([0] * 16384, [1] * 16384, list(range(16384)), [[-1]] * 16384, 64, 16384)
     # a page of the pool or of the table that is no page
     check_tables([4, 0], [4, 3], [-1, 6], [[-1, 0], [0, 0]], 4, 7)
+
+
+@pytest.mark.parametrize("B", [4070, 4075, 4090, 4095, 4096])
+def test_page_tables_sequences_that_fill_48_kb(B):
+    # 12 bytes a sequence and the block's fixed part: below, at and above what a block has
+    # without asking for more (in a process of its own: asking once is enough for all calls)
+    code = f"""
+import torch
+from io_aware_softmax_b200 import attn_page_tables, device_status
+e = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+slots, pos, lens, off, used = attn_page_tables(e([3] * {B}), e([1] * {B}), e([]), e([[7]] * {B}),
+                                               page_size=64, num_tokens={B})
+assert (slots == 7 * 64 + 3).all() and (pos == 3).all() and (lens == 4).all()
+assert off.tolist() == list(range({B} + 1)) and used.item() == 0 and device_status() == 0
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr
 
 
 def test_page_tables_no_sequences():
