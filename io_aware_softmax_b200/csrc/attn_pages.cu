@@ -11,11 +11,16 @@
 // takes both sums over all sequences itself (8 bytes a sequence from L2) in one scan and keeps
 // them in shared memory, which needs no block to wait for another, and then maps its share of
 // the tokens by a binary search.  Divisions by the page size are products with its reciprocal.
-// Measured: 5.6 us for 64 sequences of one token, 9.8 us for 1.3 million tokens of 256 (16 MB).
+// Depths in drafted trees come from doubling links in shared memory, a sequence to a warp or a
+// block: their cost goes by the number of tokens, however deep the tree is.
+// Measured (replayed back to back): 5.9 us for 64 sequences of one token, 10.0 us for 1.3 million
+// tokens of 256 (16 MB), 6.5 us for 37 trees of up to 60 nodes; a chain of 8192 given by its
+// parents beside 16 trees of 40: 35 us, where a walk through each token's ancestors took 1.4 ms.
 // A page taken in this call is read from the free list, never from the table entry another
 // block may be writing; entries of pages owned before are only read.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <climits>
 
 #include "attn_serve.h"
@@ -34,10 +39,19 @@ struct Sums {
   long long tokens, pages;
 };
 
-// A block's shared memory beside the 12 bytes a sequence.
+// A tree of up to kWarpNodes tokens is one warp's, a longer one goes through a block in chunks of
+// kChunkNodes.  16 trees of 128 nodes: 7.6 us by warps, 15.2 by blocks; of 256 nodes 9.6 and
+// 10.3; one tree of 256 alone 8.8 and 5.2.
+constexpr int kWarpNodes = 256;
+constexpr int kChunkNodes = kPagesWarps * kWarpNodes;
+
+// A block's shared memory: what every call has, and the dynamic part, of sequences and of trees.
 struct BlockShared {
   Sums warp_sums[2][kPagesWarps];
 };
+constexpr int kSmemOfSm = 228 * 1024;     // 1 KB a block is the system's
+constexpr int kTreeBytes = kChunkNodes * 8;
+constexpr int dynamic_bytes(int B, bool trees) { return (3 * B + 1) * 4 + (trees ? kTreeBytes : 0); }
 
 __device__ __forceinline__ Sums block_scan(Sums v, Sums* warp_sums, Sums& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -68,11 +82,41 @@ __device__ __forceinline__ Sums block_scan(Sums v, Sums* warp_sums, Sums& total)
   return Sums{before.tokens + x.tokens - v.tokens, before.pages + x.pages - v.pages};
 }
 
+// Doubles the links of n nodes until each names the topmost of its ancestors there (which names
+// itself, 0 steps away).  In place: whichever of its values another thread's link is read at,
+// it names an ancestor and the steps to it, and a link to a topmost node changes no more.
+// kThreads threads call it, a warp or the block, thread `me` of them.
+template <int kThreads>
+__device__ __forceinline__ void double_links(volatile unsigned* links, int n, int me) {
+  auto sync = [](bool more) -> bool {
+    if (kThreads > 32) return __syncthreads_or(more);
+    __syncwarp();
+    return __any_sync(0xffffffffu, more);
+  };
+  sync(false);
+  for (bool more = true; more;) {
+    more = false;
+    for (int i = me; i < n; i += kThreads) {
+      const unsigned mine = links[i], up = links[mine >> 16];
+      if ((up >> 16) != (mine >> 16)) {
+        links[i] = up + (mine & 0xffffu);
+        more = true;
+      }
+    }
+    more = sync(more);
+  }
+}
+
+template <bool kTrees>
 __global__ void __launch_bounds__(kPagesThreads) attn_page_tables_kernel(const PagesParams p) {
   extern __shared__ int smem[];
   int* off = smem;                  // [B + 1] first token of each sequence
   int* held = smem + p.B + 1;       // [B] cache rows before the step
   int* first = held + p.B;          // [B] free-list index of the first new page
+  // with parents: ancestor << 16 | steps to it, nodes counted from the chunk's first, and the
+  // depth of a node whose parent is none, or in an earlier chunk
+  unsigned* links = reinterpret_cast<unsigned*>(first + p.B);   // [kChunkNodes]
+  int* base = first + p.B + kChunkNodes;                        // [kChunkNodes]
   __shared__ BlockShared sh;
   const int tid = threadIdx.x;
   const int cap = p.max_pages * p.page_size;        // below 2^31 (host check)
@@ -144,7 +188,49 @@ __global__ void __launch_bounds__(kPagesThreads) attn_page_tables_kernel(const P
     return x < p.num_free ? __ldg(p.free_pages + x) : -1;
   };
 
-  // slots and positions
+  // positions of drafted trees: c + depth, the depth being the number of steps to a node without
+  // a parent (an entry that is no earlier node counts as none)
+  if (kTrees) {
+    const int lane = tid & 31, warp = tid >> 5;
+    auto place = [&](int b, int i, long long depth) {
+      p.positions[off[b] + i] = (int)min(held[b] + depth, (long long)INT_MAX);
+    };
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+      const int n = off[b + 1] - off[b];
+      if (n <= kWarpNodes) continue;
+      for (int c0 = 0; c0 < n; c0 += kChunkNodes) {
+        const int m = min(n - c0, kChunkNodes);
+        for (int i = tid; i < m; i += kPagesThreads) {
+          const int q = __ldg(p.parents + off[b] + c0 + i);
+          const bool up = q >= 0 && q < c0 + i;
+          links[i] = up && q >= c0 ? ((unsigned)(q - c0) << 16) + 1u : (unsigned)i << 16;
+          // this block has written the positions of earlier chunks
+          if (!up) base[i] = 0;
+          else if (q < c0) base[i] = p.positions[off[b] + q] - held[b] + 1;
+        }
+        double_links<kPagesThreads>(links, m, tid);
+        for (int i = tid; i < m; i += kPagesThreads) {
+          const unsigned w = links[i];
+          place(b, c0 + i, (long long)base[w >> 16] + (w & 0xffffu));
+        }
+        __syncthreads();
+      }
+    }
+    for (int b = blockIdx.x * kPagesWarps + warp; b < p.B; b += gridDim.x * kPagesWarps) {
+      const int n = off[b + 1] - off[b];
+      if (n > kWarpNodes) continue;
+      unsigned* mine = links + warp * kWarpNodes;
+      for (int i = lane; i < n; i += 32) {
+        const int q = __ldg(p.parents + off[b] + i);
+        mine[i] = q >= 0 && q < i ? ((unsigned)q << 16) + 1u : (unsigned)i << 16;
+      }
+      double_links<32>(mine, n, lane);
+      for (int i = lane; i < n; i += 32) place(b, i, mine[i] & 0xffffu);
+      __syncwarp();
+    }
+  }
+
+  // slots, and the other positions
   const long long stride = (long long)gridDim.x * kPagesThreads * kTokensPerThread;
   for (long long t0 = ((long long)blockIdx.x * kPagesThreads + tid) * kTokensPerThread;
        t0 < p.num_tokens; t0 += stride) {
@@ -182,31 +268,21 @@ __global__ void __launch_bounds__(kPagesThreads) attn_page_tables_kernel(const P
         }
         if (page >= 0) slot[u] = (long long)page * p.page_size + ((int)row - pg * p.page_size);
       }
-      int steps = i;
-      if (p.parents != nullptr) {
-        // depth in the tree: steps to a node without a parent.  A parent lies before its
-        // node (any other entry counts as none), so the walk ends after at most i steps.
-        steps = 0;
-        for (int j = i;;) {
-          const int q = __ldg(p.parents + off[b] + j);
-          if (q < 0 || q >= j) break;
-          j = q;
-          ++steps;
-        }
-      }
-      pos[u] = (int)min((long long)c + steps, (long long)INT_MAX);
+      pos[u] = (int)min(row, (long long)INT_MAX);
     }
-    if (t0 + kTokensPerThread <= p.num_tokens) {
-      *reinterpret_cast<int4*>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    const bool full = t0 + kTokensPerThread <= p.num_tokens;
+    if (full) {
+      if (!kTrees)
+        *reinterpret_cast<int4*>(p.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
       *reinterpret_cast<longlong2*>(p.slots + t0) = make_longlong2(slot[0], slot[1]);
       *reinterpret_cast<longlong2*>(p.slots + t0 + 2) = make_longlong2(slot[2], slot[3]);
-    } else {
+    }
 #pragma unroll
-      for (int u = 0; u < kTokensPerThread; ++u)
-        if (t0 + u < p.num_tokens) {
-          p.positions[t0 + u] = pos[u];
-          p.slots[t0 + u] = slot[u];
-        }
+    for (int u = 0; u < kTokensPerThread; ++u) {
+      if (t0 + u >= p.num_tokens) continue;
+      if (!full) p.slots[t0 + u] = slot[u];
+      // a tree's positions are written above
+      if (kTrees ? t0 + u >= tokens : !full) p.positions[t0 + u] = pos[u];
     }
   }
 
@@ -232,22 +308,35 @@ void page_divisor(int d, unsigned& mul, int& shift) {
 
 }  // namespace
 
-int launch_page_tables(const PagesParams& args, int num_sms, cudaStream_t stream) {
-  PagesParams p = args;
-  page_divisor(p.page_size, p.div_mul, p.div_shift);
-  const int smem = (3 * p.B + 1) * 4;
+template <bool kTrees>
+static int launch_t(const PagesParams& p, int num_sms, cudaStream_t stream) {
+  const int smem = dynamic_bytes(p.B, kTrees);
   static std::atomic<bool> ready[64];
   // without the attribute a block has 48 KB, of which the fixed part comes first
   if (smem + (int)sizeof(BlockShared) > 48 * 1024 &&
-      !allow_smem(reinterpret_cast<const void*>(attn_page_tables_kernel),
-                  (3 * kPagesMaxSeqs + 1) * 4, ready))
+      !allow_smem(reinterpret_cast<const void*>(attn_page_tables_kernel<kTrees>),
+                  dynamic_bytes(kPagesMaxSeqs, kTrees), ready))
     return -4;
   const long long per_block = kPagesThreads * kTokensPerThread;
-  long long blocks = ((long long)p.num_tokens + per_block - 1) / per_block;
-  blocks = blocks < 1 ? 1 : blocks;
-  if (blocks > 4 * num_sms) blocks = 4 * num_sms;
-  attn_page_tables_kernel<<<(unsigned)blocks, kPagesThreads, smem, stream>>>(p);
+  long long blocks = std::max(((long long)p.num_tokens + per_block - 1) / per_block, 1LL);
+  // A warp for each of a few trees; of many, the blocks for the tokens take several each (4000
+  // trees of 100 nodes: 33 us with the tokens' 250 blocks, 37 with 444).
+  if (kTrees)
+    blocks = std::max(blocks, std::min(((long long)p.B + kPagesWarps - 1) / kPagesWarps,
+                                       (long long)num_sms));
+  // Four blocks an SM, or what fits there at a time: each takes the sums of all sequences anew,
+  // and a second wave would do so one after the other.
+  const int resident = std::min(4, kSmemOfSm / (smem + (int)sizeof(BlockShared) + 1024));
+  blocks = std::min(blocks, (long long)std::max(resident, 1) * num_sms);
+  attn_page_tables_kernel<kTrees><<<(unsigned)blocks, kPagesThreads, smem, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? 0 : -4;
+}
+
+int launch_page_tables(const PagesParams& args, int num_sms, cudaStream_t stream) {
+  PagesParams p = args;
+  page_divisor(p.page_size, p.div_mul, p.div_shift);
+  return p.parents != nullptr ? launch_t<true>(p, num_sms, stream)
+                              : launch_t<false>(p, num_sms, stream);
 }
 
 }  // namespace attn

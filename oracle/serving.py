@@ -42,11 +42,16 @@ def page_tables(ctx_lens, new_lens, free_pages, block_table, page_size: int, num
         for p in range(-(-owned // page_size), -(-end // page_size)):
             table[b, p] = free_pages[used] if used < len(free_pages) else -1
             used += 1
-        mine = None if parents is None else parents[o:o + n]
+        depths = list(range(n))
+        if parents is not None:
+            mine = parents[o:o + n]
+            for i in range(n):              # a parent comes before its node
+                p = tree_parent(mine, i)
+                depths[i] = depths[p] + 1 if p >= 0 else 0
         for i in range(n):
             if c + i < cap and table[b, (c + i) // page_size] >= 0:
                 slots[o + i] = int(table[b, (c + i) // page_size]) * page_size + (c + i) % page_size
-            positions[o + i] = c + (i if parents is None else tree_depth(mine, i))
+            positions[o + i] = c + depths[i]
         seq_lens.append(end)
         offsets.append(o + n)
     return (slots, positions, np.array(seq_lens, np.int32), np.array(offsets, np.int32),

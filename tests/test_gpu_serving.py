@@ -95,7 +95,7 @@ def test_page_tables_edges():
     check_tables([4, 0], [4, 3], [-1, 6], [[-1, 0], [0, 0]], 4, 7)
 
 
-@pytest.mark.parametrize("B", [4070, 4075, 4090, 4095, 4096])
+@pytest.mark.parametrize("B", [2700, 2709, 2720, 2730, 2740, 4070, 4075, 4090, 4095, 4096])
 def test_page_tables_sequences_that_fill_48_kb(B):
     # 12 bytes a sequence and the block's fixed part: below, at and above what a block has
     # without asking for more (in a process of its own: asking once is enough for all calls)
@@ -103,10 +103,12 @@ def test_page_tables_sequences_that_fill_48_kb(B):
 import torch
 from io_aware_softmax_b200 import attn_page_tables, device_status
 e = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
-slots, pos, lens, off, used = attn_page_tables(e([3] * {B}), e([1] * {B}), e([]), e([[7]] * {B}),
-                                               page_size=64, num_tokens={B})
-assert (slots == 7 * 64 + 3).all() and (pos == 3).all() and (lens == 4).all()
-assert off.tolist() == list(range({B} + 1)) and used.item() == 0 and device_status() == 0
+for parents in (None, e([0] * {B})):
+    slots, pos, lens, off, used = attn_page_tables(
+        e([3] * {B}), e([1] * {B}), e([]), e([[7]] * {B}), page_size=64, num_tokens={B},
+        parents=parents)
+    assert (slots == 7 * 64 + 3).all() and (pos == 3).all() and (lens == 4).all()
+    assert off.tolist() == list(range({B} + 1)) and used.item() == 0 and device_status() == 0
 """
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
@@ -129,6 +131,76 @@ def test_page_tables_trees(seed):
     ctx = rng.integers(0, 500, 9)
     check_tables(ctx.tolist(), new.tolist(), list(range(100)), [[0] * 20] * 9, 32,
                  len(parents), parents=parents.tolist())
+
+
+def _parents(kind, n, rng):
+    i = np.arange(n)
+    if kind == "chain":
+        return i - 1
+    if kind == "near":
+        return i - 1 - np.minimum(rng.integers(0, 3, n), i)
+    if kind == "far":                       # anywhere before, across many chunks
+        return rng.integers(-1, np.maximum(i, 1))
+    if kind == "combs":                     # long lines that hang on early nodes, and bad entries
+        p = i - 1
+        at = rng.integers(0, n, n // 300 + 1)
+        p[at] = rng.choice([-9, 0, 1, n, 2 ** 31 - 1], len(at))
+        return p
+    return np.full(n, -1)
+
+
+@pytest.mark.parametrize("kind", ["chain", "near", "far", "combs", "none"])
+@pytest.mark.parametrize("long", [255, 256, 257, 2048, 2049, 4096, 9001])
+def test_page_tables_long_trees_beside_small_ones(kind, long):
+    # sequences of one warp, of one chunk of a block, of several: small ones before and behind
+    rng = np.random.default_rng(long)
+    new = [3, 0, long, 60, 1, 300, long // 2 + 1, 17]
+    parents = np.concatenate([_parents(kind if n > 20 else "near", n, rng) for n in new] + [[0]])
+    ctx = rng.integers(0, 500, len(new))
+    T = len(parents)
+    for tokens in (T, T - 300):           # and cut within the last sequences
+        check_tables(ctx.tolist(), new, list(range(T // 64 + 30)), [[0] * 160] * len(new), 64,
+                     tokens, parents=parents[:tokens].tolist())
+
+
+def test_page_tables_many_trees():
+    # several sequences a warp, and long ones that share a block
+    rng = np.random.default_rng(4)
+    new = rng.integers(0, 12, 9000)
+    new[rng.integers(0, 9000, 40)] = 400
+    new[[5, 5 + 592, 5 + 1184]] = 3000
+    parents = np.concatenate([_parents("near", int(n), rng) for n in new])
+    check_tables([5] * 9000, new.tolist(), list(range(9999)), [[0] * 48] * 9000, 64, len(parents),
+                 parents=parents.tolist())
+
+
+def test_page_tables_time_goes_by_the_tokens_and_not_by_the_depth():
+    # a chain of 8192 through parents beside small trees; a walk of every node to its root took
+    # 270 times as long as the call without parents, and 64 of them leave room for any box
+    new = [8192] + [40] * 16
+    parents = np.concatenate([_parents("chain", n, None) for n in new])
+    T = len(parents)
+    args = (i32([100] * 17), i32(new), i32(list(range(400))), i32([[0] * 160] * 17))
+    out = dict(slots=torch.empty(T, dtype=torch.int64, device="cuda"), positions=i32([0] * T),
+               seq_lens=i32([0] * 17), token_offsets=i32([0] * 18), pages_used=i32([0]))
+
+    def timed(p):
+        attn_page_tables(*args, page_size=64, num_tokens=T, parents=p, **out)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(10):
+                attn_page_tables(*args, page_size=64, num_tokens=T, parents=p, **out)
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        best = float("inf")
+        for _ in range(5):
+            a.record()
+            graph.replay()
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+
+    assert timed(i32(parents)) <= 64 * timed(None)
 
 
 def test_page_tables_large_offsets():

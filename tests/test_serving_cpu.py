@@ -57,6 +57,18 @@ def test_tree_depth_and_bad_parents():
     assert [oracle.tree_depth(None, i) for i in range(4)] == [0, 1, 2, 3]
 
 
+def test_page_tables_positions_are_the_depths_of_the_trees():
+    rng = np.random.default_rng(6)
+    new = [40, 1, 0, 25]
+    parents = [int(rng.integers(-2, i + 2)) for n in new for i in range(n)]
+    _, pos, _, off, _, _ = oracle.page_tables([7] * 4, new, range(9), [[0] * 9] * 4, 8, 66,
+                                              parents=parents)
+    for b, n in enumerate(new):
+        mine = parents[off[b]:off[b + 1]]
+        assert pos[off[b]:off[b + 1]].tolist() == [7 + oracle.tree_depth(mine, i)
+                                                   for i in range(n)]
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_rotation_is_the_complex_product(interleaved):
     rng = np.random.default_rng(0)
