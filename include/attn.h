@@ -341,8 +341,8 @@ ATTN_API int attn_page_tables(const int* ctx_lens, const int* new_lens, const in
  *   rope_table  fp32 [table_rows, rot], row p: cos of the rot / 2 angles of position p, then
  *            their sin (compute the angles in 64 bits: those of far positions do not fit 32).
  *            rot a multiple of 16, at most d; 0: no rotation
- *   positions   int32 [B, N], or NULL: row n has position n.  A position outside
- *            [0, table_rows) reads a table row of zeros.
+ *   positions   int32 [B, N]; one outside [0, table_rows) reads a table row of zeros.  NULL: row n
+ *            has position n, and with a rotation table_rows is at least N (else INVALID_ARG)
  *   interleaved 0: pair i is (i, i + rot / 2); else (2 i, 2 i + 1)
  *   eps      positive and normal in fp32 (with a norm)
  * Statistics and products are fp32, outputs rounded once.  An output may not overlap an input

@@ -541,6 +541,14 @@ def _prep_inputs(qkv: torch.Tensor, dims: int, q_weight, k_weight, rope_table):
     return rot, rows
 
 
+def _positions(positions, B: int, N: int, rot: int, rows: int, qkv: torch.Tensor):
+    """Checks the positions of a training call, or that the table has those of 0..N-1."""
+    if positions is not None:
+        _given(positions, "positions", torch.int32, (B, N), qkv)
+    elif rot and rows < N and B:
+        raise ValueError(f"rope_table has {rows} rows for the positions 0 to {N - 1}")
+
+
 def attn_qk_norm_rope(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
                       k_weight: Optional[torch.Tensor], rope_table: Optional[torch.Tensor], *,
                       num_q_heads: int, positions: Optional[torch.Tensor] = None,
@@ -552,7 +560,8 @@ def attn_qk_norm_rope(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
     (q [B,Hq,N,d], k [B,Hkv,N,d], v [B,Hkv,N,d]) as attn_fwd takes them.
 
     Gains bf16 [d] (both None: no norm); rope_table fp32 [rows, rot], cos | sin of each
-    position's rot/2 angles (None: no rotation); positions int32 [B,N] (None: 0..N-1)."""
+    position's rot/2 angles (None: no rotation); positions int32 [B,N] (None: 0..N-1, which the
+    table has to have)."""
     if stream is not None:
         with torch.cuda.stream(stream):     # what the call allocates is that stream's too
             return attn_qk_norm_rope(qkv, q_weight, k_weight, rope_table,
@@ -565,7 +574,7 @@ def attn_qk_norm_rope(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
     if not 0 < Hq < H or (H - Hq) % 2:
         raise ValueError(f"{H} heads cannot be {Hq} query heads and as many key as value heads")
     Hkv = (H - Hq) // 2
-    _optional(positions, "positions", torch.int32, (B, N), qkv)
+    _positions(positions, B, N, rot, rows, qkv)
     q = _result(q, "q", torch.bfloat16, (B, Hq, N, d), qkv)
     k = _result(k, "k", torch.bfloat16, (B, Hkv, N, d), qkv)
     v = _result(v, "v", torch.bfloat16, (B, Hkv, N, d), qkv)
@@ -604,7 +613,7 @@ def attn_qk_norm_rope_bwd(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
     _given(dq, "dq", bf16, (B, Hq, N, d), qkv)
     _given(dk, "dk", bf16, (B, Hkv, N, d), qkv)
     _given(dv, "dv", bf16, (B, Hkv, N, d), qkv)
-    _optional(positions, "positions", torch.int32, (B, N), qkv)
+    _positions(positions, B, N, rot, rows, qkv)
     dqkv = _result(dqkv, "dqkv", bf16, qkv.shape, qkv)
     ws_bytes = 0
     if q_weight is None:

@@ -724,6 +724,8 @@ static int check_prep(PrepParams& p, const void* qkv, const void* q_weight, cons
   if (tokens > 0 && H > 0) {
     if (qkv == nullptr || (rot > 0 && table_rows > 0 && rope_table == nullptr))
       return ATTN_ERR_INVALID_ARG;
+    // without positions they are 0 to N - 1, and all of them have to be in the table
+    if (rot > 0 && positions == nullptr && table_rows < N) return ATTN_ERR_INVALID_ARG;
     if (!aligned16(qkv) || !aligned16(q_weight) || !aligned16(k_weight) || !aligned16(rope_table) ||
         (reinterpret_cast<uintptr_t>(positions) & 3u))
       return ATTN_ERR_MISALIGNED;

@@ -249,6 +249,22 @@ def test_qk_norm_rope_bwd_refusals(lib, change):
     assert lib.calls == []
 
 
+def test_a_table_too_short_for_the_default_positions(lib):
+    x, w, g = z((2, 5, 8, 64)), z((64,)), [z((2, h, 5, 64)) for h in (4, 2, 2)]
+    short, pos = z((4, 32), F32), z((2, 5), I32)
+    with pytest.raises(ValueError, match="4 rows"):
+        api.attn_qk_norm_rope(x, w, w, short, num_q_heads=4)
+    with pytest.raises(ValueError, match="4 rows"):
+        api.attn_qk_norm_rope_bwd(x, w, w, short, *g)
+    assert lib.calls == []
+    # positions that the host does not see, a table without angles, and nothing to rotate
+    api.attn_qk_norm_rope(x, w, w, short, num_q_heads=4, positions=pos)
+    api.attn_qk_norm_rope_bwd(x, w, w, short, *g, positions=pos)
+    api.attn_qk_norm_rope(x, w, w, z((0, 0), F32), num_q_heads=4)
+    api.attn_qk_norm_rope(x[:0], w, w, short, num_q_heads=4)
+    assert len(lib.calls) == 4
+
+
 @pytest.mark.parametrize("change", [
     dict(positions=None), dict(positions=z((8,), I32)), dict(slots=z((9,), I32)),
     dict(slots=z((8,), I64)), dict(k_pages=z((3, 2, 64, 128))), dict(v_pages=z((4, 2, 64, 64))),
@@ -331,6 +347,18 @@ def test_qk_norm_rope_status(clib):
         assert call(f, a, **{n: at(20, 8)}) == -3, n
     assert call(f, a, pos=at(30, 2)) == -3
     assert call(f, a, B=0) == 0 and call(f, a, N=0) == 0 and call(f, a, Hq=0, Hkv=0) == 0
+
+
+def test_a_table_too_short_for_the_default_positions_status(clib):
+    a = dict(qkv=at(1), wq=at(2), wk=at(3), table=at(4), pos=None, q=at(5), k=at(6), v=at(7), B=2,
+             N=5, Hq=4, Hkv=2, d=64, rot=32, rows=4, eps=1e-6, inter=0, stream=None)
+    f = clib.attn_qk_norm_rope
+    assert call(f, a) == -1 and call(f, a, rows=0) == -1 and call(f, a, table=None, rows=0) == -1
+    assert call(f, a, B=0) == 0
+    b = dict(qkv=at(1), wq=at(2), wk=at(3), table=at(4), pos=None, dq=at(5), dk=at(6), dv=at(7),
+             dqkv=at(8), dwq=at(9), dwk=at(10), B=2, N=5, Hq=4, Hkv=2, d=64, rot=32, rows=4,
+             eps=1e-6, inter=0, ws=at(11), bytes=1 << 20, stream=None)
+    assert call(clib.attn_qk_norm_rope_bwd, b) == -1
 
 
 def test_qk_norm_rope_paged_status(clib):
