@@ -88,6 +88,10 @@ struct TreeCfg {
 
 // ---------------------------------------------------------------------------- schedule
 
+// Lengths, offsets, parents and table entries are read with ordinary loads throughout: the kernels
+// are launched while the one before them, which may write those arrays, still runs, and a load
+// through the read-only path is defined only for what no one writes while the kernel lives.
+
 // Sequence b as its query rows, its rows in the cache and the units of its segments see it.
 struct Seq {
   int first, n, nodes;   // first token, drafted rows, rows computed (n, at most max_nodes)
@@ -99,10 +103,10 @@ struct Seq {
 
 __device__ __forceinline__ Seq load_seq(const TreeParams& p, int b, int block_nodes) {
   Seq s;
-  s.first = min(max(__ldg(p.offsets + b), 0), p.T);
-  s.n = max(min(__ldg(p.offsets + b + 1), p.T) - s.first, 0);
+  s.first = min(max(p.offsets[b], 0), p.T);
+  s.n = max(min(p.offsets[b + 1], p.T) - s.first, 0);
   s.nodes = min(s.n, p.max_nodes);
-  s.len = min(max(__ldg(p.seq_lens + b), 0), p.cap);
+  s.len = min(max(p.seq_lens[b], 0), p.cap);
   s.ktiles = max((int)(((unsigned)s.len + kKeys - 1) / kKeys), 1);
   s.blocks = (s.nodes + block_nodes - 1) / block_nodes;
   s.span = s.ktiles + kPieceCost;
@@ -280,6 +284,21 @@ __device__ __noinline__ unsigned __int128 visible_keys(unsigned __int128 seen, i
   return (seen << (int)-j0) | (((unsigned __int128)1 << (int)-j0) - 1);
 }
 
+// A sequence's parents into shared memory, a warp together; an entry that is no earlier node
+// becomes -1.  All loads come before the first store, which they could not pass.
+__device__ __noinline__ void load_parents(const int* parents, int nodes, int8_t* to) {
+  const int lane = threadIdx.x & 31;
+  int q[kTreeMaxNodes / 32];
+#pragma unroll
+  for (int k = 0; k < kTreeMaxNodes / 32; ++k)
+    q[k] = lane + 32 * k < nodes ? parents[lane + 32 * k] : -1;
+#pragma unroll
+  for (int k = 0; k < kTreeMaxNodes / 32; ++k) {
+    const int i = lane + 32 * k;
+    if (i < nodes) to[i] = (int8_t)((q[k] >= 0 && q[k] < i) ? q[k] : -1);
+  }
+}
+
 // Whether drafted rows [from, end) of a V tile hold an infinity or a NaN (the warp together).
 // 0 * x is NaN for those and 0 for the rest: one instruction a pair of values.
 template <int kChunks>
@@ -348,7 +367,7 @@ __device__ __noinline__ void patch_rows(const TreeParams p, const Run* run) {
       const int pos = pc.s.len - pc.s.n + j;
       if (pos >= k0 && pos < k1) {
         const int pg = pos / p.page_size;
-        const int page = __ldg(p.block_table + (size_t)pc.b * p.max_pages + pg);
+        const int page = p.block_table[(size_t)pc.b * p.max_pages + pg];
         // a page outside the cache reads zeros
         if ((unsigned)page < (unsigned)p.num_pages) {
           const __nv_bfloat16* v =
@@ -363,7 +382,7 @@ __device__ __noinline__ void patch_rows(const TreeParams p, const Run* run) {
           }
         }
       }
-      const int q = p.parents == nullptr ? j - 1 : __ldg(p.parents + pc.s.first + j);
+      const int q = p.parents == nullptr ? j - 1 : p.parents[pc.s.first + j];
       j = q < j ? q : -1;
     }
   });
@@ -444,7 +463,8 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         make_uint4(0u, 0u, 0u, 0u);
   }
   fence_proxy_async_smem();
-  // launched while the kernel before it ends: nothing of memory is read or written before this
+  // Launched while the kernel before it ends: of memory only the wait limit is read before this (its
+  // setter synchronises the device), and nothing is written.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Run run = plan_run(p, block_nodes, reinterpret_cast<long long*>(base + C::kStart + 32),
                            reinterpret_cast<Run*>(base + C::kStart));
@@ -478,7 +498,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             Half x{p.num_pages * p.Hkv, 0};
             if (k < pc.s.len) {
               const int pg = k / p.page_size;
-              const int page = __ldg(table + pg);
+              const int page = table[pg];
               if ((unsigned)page < (unsigned)p.num_pages) x.z = page * p.Hkv + pc.hk;
               x.row = k - pg * p.page_size;
             }
@@ -739,10 +759,7 @@ attn_tree_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         }
         if (p.parents != nullptr && busy && masked_from < tiles) {
           // the parents of a piece that reaches the drafted rows, for its masked tiles
-          for (int i = lane; i < s.nodes; i += 32) {
-            const int q = __ldg(p.parents + s.first + i);
-            par[i] = (int8_t)((q >= 0 && q < i) ? q : -1);
-          }
+          load_parents(p.parents + s.first, s.nodes, par);
         }
         __syncwarp();
         if (lane == 0) {
@@ -963,7 +980,7 @@ __global__ void __launch_bounds__(256) attn_tree_join_kernel(const TreeParams p,
   int lo = 0, hi = p.B - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(p.offsets + mid) <= token) lo = mid; else hi = mid - 1;
+    if (p.offsets[mid] <= token) lo = mid; else hi = mid - 1;
   }
   const int block_nodes = p.tile_nodes * tiles;
   const Seq s = load_seq(p, lo, block_nodes);

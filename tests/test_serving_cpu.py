@@ -1,6 +1,7 @@
 """The operators around the attention kernels, on the CPU: their plain definitions held to
 worked examples, closed forms and differences, and the refusals of the binding and the C ABI."""
 import ctypes
+import os
 
 import numpy as np
 import pytest
@@ -292,6 +293,19 @@ def test_decode_tree_refusals(lib, change):
     with pytest.raises((ValueError, TypeError)):
         api.attn_decode_tree(**a)
     assert lib.calls == []
+
+
+# ------------------------------------------------------------------------- the sources
+
+def test_kernels_that_start_early_read_with_ordinary_loads():
+    # a kernel launched while the one before it runs may not read what that one writes through
+    # the read-only path, whose loads the compiler may also move above the wait
+    early = [s for s in build.SOURCES
+             if "griddepcontrol.wait" in open(os.path.join(build.CSRC, s)).read()]
+    assert early == ["attn_tree.cu"]
+    for s in early:
+        text = open(os.path.join(build.CSRC, s)).read()
+        assert "__ldg" not in text and "ld.global.nc" not in text, s
 
 
 # -------------------------------------------------------------------------- the C ABI
