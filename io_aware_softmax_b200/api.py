@@ -462,6 +462,14 @@ def _result(t, name: str, dtype: torch.dtype, shape, ref: torch.Tensor) -> torch
     return t
 
 
+def _on_stream(stream, ref: torch.Tensor):
+    """Makes a given stream current: what the call allocates is that stream's too.  A stream of
+    another device would leave the call on that device's current one."""
+    if isinstance(ref, torch.Tensor) and stream.device != ref.device:
+        raise ValueError(f"the stream is on {stream.device}, the inputs on {ref.device}")
+    return torch.cuda.stream(stream)
+
+
 def attn_page_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor,
                      block_table: torch.Tensor, *, page_size: int, num_tokens: int,
                      free_used: Optional[torch.Tensor] = None,
@@ -481,7 +489,7 @@ def attn_page_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages:
     earlier step on the same free list; ``held_rows`` (int32 [B]) are the rows that already
     have pages, where rejected drafts made them more than ctx_lens."""
     if stream is not None:
-        with torch.cuda.stream(stream):     # what the call allocates is that stream's too
+        with _on_stream(stream, ctx_lens):
             return attn_page_tables(
                 ctx_lens, new_lens, free_pages, block_table, page_size=page_size,
                 num_tokens=num_tokens, free_used=free_used, held_rows=held_rows, parents=parents,
@@ -563,7 +571,7 @@ def attn_qk_norm_rope(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
     position's rot/2 angles (None: no rotation); positions int32 [B,N] (None: 0..N-1, which the
     table has to have)."""
     if stream is not None:
-        with torch.cuda.stream(stream):     # what the call allocates is that stream's too
+        with _on_stream(stream, qkv):
             return attn_qk_norm_rope(qkv, q_weight, k_weight, rope_table,
                                      num_q_heads=num_q_heads, positions=positions, eps=eps,
                                      interleaved=interleaved, q=q, k=k, v=v)
@@ -598,7 +606,7 @@ def attn_qk_norm_rope_bwd(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
     """Backward of attn_qk_norm_rope: (dqkv bf16 as qkv, dq_weight fp32 [d], dk_weight fp32 [d])
     from qkv and attn_bwd's (dq, dk, dv); the gains' gradients are None without a norm."""
     if stream is not None:
-        with torch.cuda.stream(stream):     # what the call allocates is that stream's too
+        with _on_stream(stream, qkv):
             return attn_qk_norm_rope_bwd(
                 qkv, q_weight, k_weight, rope_table, dq, dk, dv, positions=positions, eps=eps,
                 interleaved=interleaved, dqkv=dqkv, dq_weight=dq_weight, dk_weight=dk_weight,
@@ -653,7 +661,7 @@ def attn_qk_norm_rope_paged(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
     writes the K and V rows of each token into pages [num_pages,Hkv,page_size,d] at its slot
     (int64 [T]; a slot outside the cache writes nothing).  positions int32 [T]."""
     if stream is not None:
-        with torch.cuda.stream(stream):     # what the call allocates is that stream's too
+        with _on_stream(stream, qkv):
             return attn_qk_norm_rope_paged(
                 qkv, q_weight, k_weight, rope_table, positions, slots, k_pages, v_pages, eps=eps,
                 interleaved=interleaved, q=q)
@@ -700,7 +708,7 @@ def attn_decode_tree(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
     parents int32 [T]: index within the sequence of the node each token hangs on, -1 for the
     context; None: a chain.  Rows behind token_offsets[B] are left as they were."""
     if stream is not None:
-        with torch.cuda.stream(stream):     # what the call allocates is that stream's too
+        with _on_stream(stream, q):
             return attn_decode_tree(
                 q, k_pages, v_pages, block_table, seq_lens, token_offsets, max_nodes=max_nodes,
                 parents=parents, scale=scale, workspace=workspace, out=out, lse=lse)

@@ -295,6 +295,27 @@ def test_decode_tree_refusals(lib, change):
     assert lib.calls == []
 
 
+def test_a_stream_of_another_device_is_refused(lib):
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 7
+
+    x, w, i = z((5, 8, 64)), z((64,)), z((5,), I32)
+    pages = z((3, 2, 64, 64))
+    g = [z((1, h, 5, 64)) for h in (4, 2, 2)]
+    for call in (
+            lambda: api.attn_page_tables(i, i, i, z((5, 7), I32), page_size=64, num_tokens=5,
+                                         stream=Stream()),
+            lambda: api.attn_qk_norm_rope(x[None], w, w, None, num_q_heads=4, stream=Stream()),
+            lambda: api.attn_qk_norm_rope_bwd(x[None], w, w, None, *g, stream=Stream()),
+            lambda: api.attn_qk_norm_rope_paged(x, w, w, None, i, i.long(), pages, pages,
+                                                stream=Stream()),
+            lambda: api.attn_decode_tree(x, pages, pages, z((5, 7), I32), i, z((6,), I32),
+                                         max_nodes=4, stream=Stream())):
+        with pytest.raises(ValueError, match="stream is on cuda:1"):
+            call()
+    assert lib.calls == []
+
+
 # ------------------------------------------------------------------------- the sources
 
 def test_kernels_that_start_early_read_with_ordinary_loads():
