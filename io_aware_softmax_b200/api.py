@@ -462,6 +462,12 @@ def _result(t, name: str, dtype: torch.dtype, shape, ref: torch.Tensor) -> torch
     return t
 
 
+def _fits(*sizes: int):
+    """The library's sizes are 32-bit integers; a larger one would be cut off on its way there."""
+    if max(sizes) > 0x7fffffff or min(sizes) < -0x80000000:
+        raise ValueError(f"a size of {max(sizes, key=abs)} does not fit 32 bits")
+
+
 def _on_stream(stream, ref: torch.Tensor):
     """Makes a given stream current: what the call allocates is that stream's too.  A stream of
     another device would leave the call on that device's current one."""
@@ -503,6 +509,8 @@ def attn_page_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages:
         raise ValueError("num_tokens must not be negative")
     num_free, = _dims(free_pages, "free_pages", i32, 1)
     _, max_pages = _dims(block_table, "block_table", i32, 2)
+    page_size = int(page_size)
+    _fits(T, num_free, B, max_pages, page_size)
     _given(free_pages, "free_pages", i32, (num_free,), ctx_lens)
     _given(block_table, "block_table", i32, (B, max_pages), ctx_lens)
     _given(new_lens, "new_lens", i32, (B,), ctx_lens)
@@ -526,7 +534,7 @@ def attn_page_tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, free_pages:
         st = lib.attn_page_tables(_ptr(ctx_lens), _ptr(new_lens), _ptr(free_pages),
                                   _ptr(free_used), _ptr(held_rows), _ptr(parents),
                                   _ptr(block_table), _ptr(slots), _ptr(positions),
-                                  _ptr(seq_lens), _ptr(token_offsets), _ptr(pages_used), B, max_pages, int(page_size),
+                                  _ptr(seq_lens), _ptr(token_offsets), _ptr(pages_used), B, max_pages, page_size,
                                   num_free, T, _stream(ctx_lens.device))
     _check(st, "attn_page_tables")
     return slots, positions, seq_lens, token_offsets, pages_used
@@ -546,6 +554,7 @@ def _prep_inputs(qkv: torch.Tensor, dims: int, q_weight, k_weight, rope_table):
     _need(rope_table, "rope_table", torch.float32, 2)
     _same_device(qkv, (rope_table, "rope_table"))
     rows, rot = rope_table.shape
+    _fits(rows, rot)
     return rot, rows
 
 
@@ -579,6 +588,7 @@ def attn_qk_norm_rope(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
     rot, rows = _prep_inputs(qkv, 4, q_weight, k_weight, rope_table)
     B, N, H, d = qkv.shape
     Hq = int(num_q_heads)
+    _fits(B, N, H, d)
     if not 0 < Hq < H or (H - Hq) % 2:
         raise ValueError(f"{H} heads cannot be {Hq} query heads and as many key as value heads")
     Hkv = (H - Hq) // 2
@@ -616,6 +626,7 @@ def attn_qk_norm_rope_bwd(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
     B, N, H, d = qkv.shape
     bf16 = torch.bfloat16
     Hq, Hkv = _dims(dq, "dq", bf16, 4)[1], _dims(dk, "dk", bf16, 4)[1]
+    _fits(B, N, H, Hkv, d)
     if Hq + 2 * Hkv != H:
         raise ValueError(f"dq and dk have {Hq} and {Hkv} heads, qkv {H}")
     _given(dq, "dq", bf16, (B, Hq, N, d), qkv)
@@ -670,6 +681,7 @@ def attn_qk_norm_rope_paged(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
     T, H, d = qkv.shape
     bf16 = torch.bfloat16
     num_pages, Hkv, page_size, _ = _dims(k_pages, "k_pages", bf16, 4)
+    _fits(T, H, num_pages, Hkv, page_size, d)
     shape = (num_pages, Hkv, page_size, d)
     _given(k_pages, "k_pages", bf16, shape, qkv)
     _given(v_pages, "v_pages", bf16, shape, qkv)
@@ -718,6 +730,8 @@ def attn_decode_tree(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
     T, Hq, d = q.shape
     num_pages, Hkv, page_size, _ = _dims(k_pages, "k_pages", bf16, 4)
     B, max_pages = _dims(block_table, "block_table", i32, 2)
+    max_nodes = int(max_nodes)
+    _fits(T, Hq, num_pages, Hkv, page_size, B, max_pages, max_nodes, d)
     shape = (num_pages, Hkv, page_size, d)
     _given(k_pages, "k_pages", bf16, shape, q)
     _given(v_pages, "v_pages", bf16, shape, q)
@@ -726,7 +740,7 @@ def attn_decode_tree(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
     _given(token_offsets, "token_offsets", i32, (B + 1,), q)
     _optional(parents, "parents", i32, (T,), q)
     if workspace is None:
-        ws_bytes = int(lib.attn_decode_tree_workspace_bytes(B, Hq, Hkv, int(max_nodes), d,
+        ws_bytes = int(lib.attn_decode_tree_workspace_bytes(B, Hq, Hkv, max_nodes, d,
                                                             _index(q)))
         workspace = q.new_empty(max(ws_bytes, 16), dtype=torch.uint8)
     else:
@@ -737,7 +751,7 @@ def attn_decode_tree(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tens
         st = lib.attn_decode_tree(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table),
                                   _ptr(seq_lens), _ptr(token_offsets), _ptr(parents), _ptr(out),
                                   _ptr(lse), B, T, Hq, Hkv, num_pages, page_size, max_pages,
-                                  int(max_nodes), d, float(scale or 0.0), _ptr(workspace),
+                                  max_nodes, d, float(scale or 0.0), _ptr(workspace),
                                   ws_bytes, _stream(q.device))
     _check(st, "attn_decode_tree")
     return out, lse

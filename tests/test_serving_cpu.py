@@ -295,6 +295,38 @@ def test_decode_tree_refusals(lib, change):
     assert lib.calls == []
 
 
+def test_sizes_past_32_bits_are_refused(lib):
+    # 2^32 + 64 cut to 32 bits would be 64, a size that the library takes
+    big = 2 ** 32 + 64
+    m = lambda shape, t=BF16: z(shape, t, device="meta")  # noqa: E731
+    i = m((3,), I32)
+    tables = lambda **k: api.attn_page_tables(  # noqa: E731
+        i, i, *(dict(free=m((9,), I32), table=m((3, 7), I32)) | k).values(), page_size=64,
+        num_tokens=5)
+    pages = lambda n, ps: m((n, 2, ps, 64))  # noqa: E731
+    tree = lambda k, nodes=4, P=7: api.attn_decode_tree(  # noqa: E731
+        m((3, 4, 64)), k, k, m((3, P), I32), i, m((4,), I32), max_nodes=nodes)
+    w = m((64,))
+    g = [m((1, h, 5, 64)) for h in (4, 2, 2)]
+    for call in (
+            lambda: tables(free=m((big,), I32)), lambda: tables(table=m((3, big), I32)),
+            lambda: api.attn_page_tables(i, i, i, m((3, 7), I32), page_size=big, num_tokens=5),
+            lambda: api.attn_page_tables(i, i, i, m((3, 7), I32), page_size=64 - 2 ** 32,
+                                         num_tokens=5),
+            lambda: api.attn_page_tables(i, i, i, m((3, 7), I32), page_size=64, num_tokens=big),
+            lambda: api.attn_qk_norm_rope(m((1, 5, 8, 64)), w, w, m((big, 64), F32),
+                                          num_q_heads=4),
+            lambda: api.attn_qk_norm_rope(m((1, 5, 8, big)), None, None, None, num_q_heads=4),
+            lambda: api.attn_qk_norm_rope_bwd(m((1, 5, 8, 64)), w, w, m((big, 64), F32), *g),
+            lambda: api.attn_qk_norm_rope_paged(m((3, 8, 64)), w, w, None, i, i.long(),
+                                                pages(big, 64), pages(big, 64)),
+            lambda: tree(pages(3, big)), lambda: tree(pages(big, 64)),
+            lambda: tree(pages(3, 64), nodes=2 ** 32 + 4), lambda: tree(pages(3, 64), P=big)):
+        with pytest.raises(ValueError, match="does not fit 32 bits"):
+            call()
+    assert lib.calls == []
+
+
 def test_a_stream_of_another_device_is_refused(lib):
     class Stream:
         device, cuda_stream = torch.device("cuda", 1), 7
