@@ -927,6 +927,9 @@ extern "C" int attn_decode_tree(const void* q, const void* k_pages, const void* 
       (long long)T * Hq > (1LL << 31) - 1 ||
       Hkv > 65535 || blocks * Hkv * ((cap + 127) / 128 + 8) > (1LL << 31) - 1)
     return ATTN_ERR_UNSUPPORTED;
+  // a CTA counts its share of the units in 32 bits as well
+  if (blocks * Hkv * ((cap + 127) / 128 + 8) * std::min(B, T) > plan.grid * ((1LL << 31) - 2))
+    return ATTN_ERR_UNSUPPORTED;
   if (workspace == nullptr || workspace_bytes < plan.bytes) return ATTN_ERR_WORKSPACE;
   if (!aligned16(workspace)) return ATTN_ERR_MISALIGNED;
   const size_t row = (size_t)T * Hq, cache = (size_t)num_pages * page_size * Hkv * d * 2;

@@ -481,3 +481,13 @@ def test_decode_tree_status(clib):
     assert call(f, a, bytes=need - 1) == -6 and call(f, a, ws=None) == -6
     assert call(f, a, o=a["q"]) == -1 and call(f, a, lse=at(9, need - 16)) == -1
     assert call(f, a, T=0) == 0 and call(f, a, B=0) == 0 and call(f, a, nodes=0) == 0
+
+
+def test_decode_tree_work_past_32_bits_a_cta(clib):
+    # 40000 sequences of up to 2^30 rows: 2^24 units each, 2^39 in all
+    a = dict(q=at(1), k=at(2), v=at(3), table=at(4), lens=at(5), off=at(6), parents=None, o=at(7),
+             lse=at(8), B=40000, T=40000, Hq=4, Hkv=2, pages=3, ps=1 << 20, P=1 << 10, nodes=4,
+             d=64, scale=0.0, ws=at(9), bytes=1 << 28, stream=None)
+    assert call(clib.attn_decode_tree, a) == -2
+    # few of them with tokens
+    assert call(clib.attn_decode_tree, a, T=9, ws=None) == -6
