@@ -203,6 +203,21 @@ def test_page_tables_time_goes_by_the_tokens_and_not_by_the_depth():
     assert timed(i32(parents)) <= 64 * timed(None)
 
 
+@pytest.mark.parametrize("seed", range(4))
+def test_page_tables_trees_after_rejected_drafts(seed):
+    # the step after one whose drafts were taken back: held rows and parents together
+    rng = np.random.default_rng(40 + seed)
+    B = 11
+    new = rng.integers(0, 70, B)
+    parents = np.concatenate([rng.integers(-1, np.arange(n) + 1) for n in new] + [[-1] * 5])
+    ctx = rng.integers(0, 400, B)
+    held = ctx + rng.integers(-5, 80, B)
+    table = rng.integers(100, 200, (B, 16))
+    for T in (len(parents), len(parents) - 40):
+        check_tables(ctx.tolist(), new.tolist(), list(range(60)), table.tolist(), 32, T, used=7,
+                     parents=parents[:T].tolist(), held=held.tolist())
+
+
 def test_page_tables_large_offsets():
     # slots past 2^31: a page number near 2^31 times its size
     slots, *_ = attn_page_tables(i32([0]), i32([65]), i32([2 ** 31 - 2, 2 ** 30]), i32([[0, 0]]),
@@ -363,6 +378,66 @@ def test_qk_norm_rope_bwd_many_blocks():
     # chain of a thread's own rows, then at most 300 more steps; |dz x r| averages below 1.1
     for got, ref, h in ((dwq, wq, Hq), (dwk, wk, Hkv)):
         within(got, ref, 400 * U * 1.1 * B * N * h * np.ones(d), "gain")
+
+
+def _bwd64(x, w, table, pos, g, eps):
+    """dqkv, the gains' gradients, and what their roundings scale with, in 64 bits on the GPU (the
+    halves' pairing, all of d rotated): x [T, H, d], g three of [T, heads, d]."""
+    Hq, Hkv = g[0].shape[1], g[1].shape[1]
+    c, s = table.double()[pos][:, None].chunk(2, -1)
+    turn = lambda a, b, c, s: torch.cat([a * c + b * s, b * c - a * s], -1)  # noqa: E731
+    dx, mag, gains, sums = [], [], [], []
+    for lo, dy, gain in ((0, g[0], w[0]), (Hq, g[1], w[1])):
+        xs, dy = x[:, lo:lo + dy.shape[1]].double(), dy.double()
+        dz = turn(*dy.chunk(2, -1), c, s)
+        a, b = dy.abs().chunk(2, -1)
+        m = torch.cat([a + b, a + b], -1)
+        r = (xs.square().mean(-1, keepdim=True) + eps).rsqrt()
+        t = dz * gain.double()
+        dx.append(r * (t - xs * r * r * (xs * t).mean(-1, keepdim=True)))
+        gains.append((dz * xs * r).sum((0, 1)))
+        sums.append((m * xs.abs() * r).sum((0, 1)))
+        t = m * gain.double().abs()
+        mag.append(r * (t + xs.abs() * r * r * (xs.abs() * t).mean(-1, keepdim=True)))
+    dx.append(g[2].double())
+    mag.append(torch.zeros_like(dx[-1]))
+    return torch.cat(dx, 1), torch.cat(mag, 1), gains, sums
+
+
+def _check_bwd(x, w, table, g, eps, tokens_at_once):
+    """Every value of the backward for x [B, N, H, d] and the default positions."""
+    B, N, H, d = x.shape
+    dx, dwq, dwk = attn_qk_norm_rope_bwd(x, *w, table, *g, eps=eps)
+    assert device_status() == 0
+    gains, sums = [0, 0], [0, 0]
+    for b in range(B):
+        for n in range(0, N, tokens_at_once):
+            at = slice(n, min(n + tokens_at_once, N))
+            pos = torch.arange(at.start, at.stop, device="cuda")
+            want, mag, gw, gs = _bwd64(x[b, at], w, table, pos,
+                                       [t[b][:, at].transpose(0, 1) for t in g], eps)
+            bad = ~((dx[b, at].double() - want).abs()
+                    <= BF * want.abs() + 40 * U * mag + 2.0 ** -133)
+            assert not bad.any(), (b, n, bad.nonzero()[:4].tolist())
+            gains = [a + v for a, v in zip(gains, gw)]
+            sums = [a + v for a, v in zip(sums, gs)]
+    # a thread adds its share of the rows in one chain (8 warps a block, 256 / d rows a warp)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for got, want, s, t in ((dwq, gains[0], sums[0], g[0]), (dwk, gains[1], sums[1], g[1])):
+        chain = 1.1 * B * N * t.shape[1] / (2 * sms * 8 * 256 / d)
+        assert ((got.double() - want).abs() <= (chain + 340) * U * s).all()
+
+
+@pytest.mark.parametrize("case", [
+    # many trips of every warp through the ring of copies: 8 steps a chunk, a chunk of one head
+    # behind a full one; the 8-step form with full chunks; 4 rows a warp; few heads
+    (2, 4003, 17, 3, 128), (1, 6007, 32, 8, 128), (1, 9001, 40, 5, 64), (3, 5001, 3, 1, 64),
+    (2, 4001, 13, 13, 128), (1, 7001, 6, 2, 128)])
+def test_qk_norm_rope_bwd_every_value_over_many_trips(case):
+    B, N, Hq, Hkv, d = case
+    x, w, table = prep_inputs(B * N, Hq, Hkv, d, d, True, N, rows=N)
+    g = [randn((B, h, N, d), 83, i) for i, h in enumerate((Hq, Hkv, Hkv))]
+    _check_bwd(x.view(B, N, -1, d), w, table, g, 1e-6, 1024)
 
 
 PAGED = [(1, 1, 1, 64, 64, 64, True, False), (16, 32, 8, 128, 64, 128, True, False),
@@ -668,6 +743,18 @@ def test_qk_norm_rope_past_32_bit_offsets():
         within(dx[b, at], want, BF * np.abs(want) + 40 * U * 32, "dqkv")
 
 
+def test_qk_norm_rope_bwd_every_value_past_32_bit_offsets():
+    B, N, Hq, Hkv, d = 3, 61440 + 3, 64, 16, 128
+    gen = torch.Generator(device="cuda").manual_seed(96)
+    rand = lambda *s: torch.randn(s, device="cuda", dtype=torch.bfloat16,  # noqa: E731
+                                  generator=gen)
+    x = rand(B, N, Hq + 2 * Hkv, d)
+    assert x.numel() > 2 ** 31
+    w = tuple((1 + 0.3 * randn((d,), 97, k).float()).bfloat16() for k in (1, 2))
+    g = [rand(B, h, N, d) for h in (Hq, Hkv, Hkv)]
+    _check_bwd(x, w, rope(N, d), g, 1e-6, 4096)
+
+
 def test_tree_pages_outside_the_cache_read_zeros():
     q, kp, vp, table, offsets, par = tree_inputs([200, 100], [3, 4], 4, 2, 64, 64, 15)
     table[0, 1], table[1, 0] = -1, kp.shape[0]
@@ -691,6 +778,85 @@ def test_tree_of_one_node_is_the_paged_decode():
     # the two kernels round the weights alike but at other maxima
     assert (o1 - o2.squeeze(2)).abs().max().item() <= 2e-2
     assert (l1 - l2.squeeze(2)).abs().max().item() <= 1e-4
+
+
+def test_tree_calls_back_to_back_on_one_workspace():
+    # each call's kernels are launched while those of the call before still read the workspace:
+    # cut segments, other lengths, offsets, batch sizes and widths, nothing else between
+    shapes = [([3000, 1777, 20, 2600], [6, 9, 3, 1], 9), ([9000], [7], 9),
+              ([40, 5000, 700], [40, 31, 40], 40), ([130] * 30, [2] * 30, 9),
+              ([4000, 0, 4100, 60], [33, 0, 40, 12], 64), ([12000, 11], [1, 4], 4)]
+    calls, bytes_ = [], 0
+    for i, (lens, n, nodes) in enumerate(shapes):
+        q, kp, vp, table, offsets, par = tree_inputs(lens, n, 16, 4, 128, 64, 200 + i)
+        calls.append(((q, kp, vp, i32(table), i32(lens), i32(offsets)),
+                      dict(max_nodes=nodes, parents=i32(par))))
+        bytes_ = max(bytes_, attn_decode_tree_workspace_bytes(len(lens), 16, 4, nodes, 128))
+    ws = torch.empty(bytes_, dtype=torch.uint8, device="cuda")
+    alone = []
+    for (args, kw), (lens, n, nodes) in zip(calls, shapes):
+        o, lse = attn_decode_tree(*args, **kw)
+        torch.cuda.synchronize()
+        O, L, A = oracle.decode_tree(*(f64(t) for t in args[:3]), args[3].cpu().numpy(), lens,
+                                     args[5].tolist(), kw["parents"].tolist())
+        within(o, O, 1.02 * BF * (np.abs(O) + A), "O")
+        assert np.abs(f64(lse) - L).max(initial=0) <= 1e-4
+        alone.append((o, lse))
+    order = np.random.default_rng(0).integers(0, len(calls), 60).tolist()
+    outs = [tuple(torch.full_like(t, 7) for t in alone[i]) for i in order]
+
+    def run():
+        for i, (o, lse) in zip(order, outs):
+            args, kw = calls[i]
+            attn_decode_tree(*args, **kw, out=o, lse=lse, workspace=ws)
+
+    def check():
+        torch.cuda.synchronize()
+        assert device_status() == 0
+        for k, (i, got) in enumerate(zip(order, outs)):
+            for a, b in zip(got, alone[i]):
+                assert torch.equal(a, b), (k, i)
+                a.fill_(7)
+
+    run()
+    check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(3):
+        graph.replay()
+        check()
+
+
+def test_tree_replayed_with_far_fewer_nodes_than_the_graph_was_captured_for():
+    B, most, T = 5, 100, 320
+    q, kp, vp, table, _, _ = tree_inputs([700] * B, [1] * B, 8, 2, 128, 64, 19,
+                                         spare_rows=T - B)
+    lens, offsets, parents = i32([0] * B), i32([0] * (B + 1)), i32([-1] * T)
+    out, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], device="cuda")
+    ws = torch.empty(attn_decode_tree_workspace_bytes(B, 8, 2, most, 128), dtype=torch.uint8,
+                     device="cuda")
+    args = (q, kp, vp, i32(table), lens, offsets)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        attn_decode_tree(*args, max_nodes=most, parents=parents, out=out, lse=lse, workspace=ws)
+    rng = np.random.default_rng(19)
+    for n in ([1, 1, 1, 1, 1], [4, 0, 7, 2, 5], [100, 3, 0, 33, 100], [0] * 5, [32, 33, 31, 64, 1]):
+        L = [int(v) for v in rng.integers(100, 700, B)]
+        off = np.concatenate([[0], np.cumsum(n)])
+        par = [max(-1, i - 1 - int(rng.integers(3))) for m in n for i in range(m)]
+        for t, v in ((lens, L), (offsets, off), (parents, par + [0] * (T - len(par)))):
+            t.copy_(i32(v))
+        out.fill_(7), lse.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert device_status() == 0
+        m = int(off[-1])
+        O, W, A = oracle.decode_tree(f64(q), f64(kp), f64(vp), table, L, off,
+                                     par + [0] * (T - len(par)))
+        within(f64(out)[:m], O[:m], 1.02 * BF * (np.abs(O) + A)[:m], "O")
+        assert np.abs(f64(lse)[:m] - W[:m]).max(initial=0) <= 1e-4
+        assert (out[m:] == 7).all() and (lse[m:] == 7).all()
 
 
 # ------------------------------------------------------------------- a step of serving
