@@ -316,6 +316,7 @@ ATTN_API int attn_decode_merge(const float* o_part, const float* lse_part, void*
  *               the int32 arrays 4-byte aligned)
  *   seq_lens int32 [B], token_offsets int32 [B + 1], pages_used int32 [1]   (written)
  *   num_tokens  capacity of slots and positions; tokens beyond it get no place
+ *   page_size   any positive size (the attention entry points take multiples of 64)
  * An output may not overlap an input or another output (INVALID_ARG): to chain steps, give
  * seq_lens and pages_used of one step to the next as ctx_lens and free_used, and other
  * arrays to write.
@@ -400,6 +401,9 @@ ATTN_API int attn_qk_norm_rope_paged(const void* qkv, const void* q_weight, cons
  * their K and V are the LAST n of the sequence's seq_lens[b] cache rows, in the same order.
  * Node i sees the rows [0, seq_lens[b] - n), and row seq_lens[b] - n + j for j = i and for
  * every ancestor j of i.
+ * Rows stay where they were written: if the accepted path of a tree is not its first nodes in
+ * order, the caller moves that path's K and V rows together, to the rows from seq_lens[b] - n on,
+ * before the next step counts them as context.
  *
  *   q        bf16 [T, Hq, d]                o  bf16 [T, Hq, d], lse fp32 [T, Hq] (written)
  *   k_pages, v_pages, block_table, page_size, max_pages_per_seq, seq_lens   as
@@ -412,7 +416,8 @@ ATTN_API int attn_qk_norm_rope_paged(const void* qkv, const void* q_weight, cons
  *   max_nodes  largest n of the call, at most 128; of a longer sequence only the first
  *            max_nodes tokens are computed
  *   workspace, workspace_bytes  device scratch, 16-byte aligned, of
- *            attn_decode_tree_workspace_bytes bytes
+ *            attn_decode_tree_workspace_bytes bytes; calls that may run at the same time (on
+ *            two streams, in two graphs) need one each
  * Rows of q behind token_offsets[B], and between a sequence's max_nodes and its end, are
  * left as they were in o and lse.  A node that sees no row (seq_lens below n) gets O = 0 and
  * LSE = -inf.  What a page holds past the sequence's end is not used, whatever it is, and an

@@ -513,7 +513,13 @@ __global__ void __launch_bounds__(1024) attn_qk_prep_dw_kernel(const float* part
 }
 
 // Steps of a chunk: many for a large call, so that the angles are read and multiplied seldom,
-// fewer while that leaves SMs without warps.
+// fewer while that leaves SMs with fewer than 16 warps.  With 4, 8, 16, 32 and 64 warps an SM for
+// the 16 (us):
+//   200 tokens of 32 + 2 x 8 heads of 128, paged     4.0   4.0   3.8   4.7   4.9
+//   800 tokens                                       5.6   5.8   5.7   6.5   8.0
+//   backward, 250 tokens                            11.0   9.9   9.2   9.7   9.4
+//   backward, 1000 tokens                           14.2  14.1  14.1  14.6  15.8
+//   500 tokens of 32 + 2 x 32 heads                  5.9   5.9   6.0   7.2   9.5
 int chunk_steps(long long tokens, int Hq, int Hkv, int warp_rows, int num_sms) {
   int steps = kChunkSteps;
   while (steps > 1 &&

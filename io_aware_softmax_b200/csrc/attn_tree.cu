@@ -53,9 +53,14 @@ constexpr uint32_t kTreeRegsSoftmax = 192;
 constexpr uint32_t kTreeRegsOther = 112;
 constexpr int kKeys = 128;                    // keys of a tile
 // What a segment costs beside its key tiles (the first and last tile's latencies, its output),
-// in tiles: without it a CTA that gets many short segments ends long after the others.  7
-// sequences of 16 KV heads, one of them new and the others of 2500 to 5000 rows: 64 us with 0,
-// 55 with 1, 45 with 2 and 3, 46 with 4.
+// in tiles: without it a CTA that gets many short segments ends long after the others.  With 0, 1,
+// 2, 3 and 4 (us):
+//   7 sequences of up to 5000 rows, one of them new, 16 KV heads    57   47   39   40   40
+//   8 of up to 8192 rows, 8 KV heads, up to 256 query rows          80   72   63   63   63
+//   8 of up to 8192 rows, 8 KV heads, up to 64 query rows           59   45   42   42   41
+//   16 of up to 32768 rows, 8 KV heads, up to 64 query rows        279  268  259  258  258
+//   64 of up to 1500 rows, 8 KV heads, up to 32 query rows          76   73   69   69   69
+//   20 of up to 6000 rows, 8 KV heads, up to 64 query rows, d 64    73   66   55   53   53
 constexpr int kPieceCost = 2;
 constexpr float kTreeThreshold = 8.0f;        // O is rescaled when its max grows by 2^8
 constexpr float kTreeLn2 = 0.69314718055994531f;
