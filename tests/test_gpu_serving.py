@@ -176,7 +176,7 @@ def test_page_tables_many_trees():
 
 def test_page_tables_time_goes_by_the_tokens_and_not_by_the_depth():
     # a chain of 8192 through parents beside small trees; a walk of every node to its root took
-    # 270 times as long as the call without parents, and 64 of them leave room for any box
+    # 270 times as long as the call without parents; 64 times leave room for noise
     new = [8192] + [40] * 16
     parents = np.concatenate([_parents("chain", n, None) for n in new])
     T = len(parents)
